@@ -62,7 +62,8 @@ typedef enum {
     KDA_ERR_UNSUPPORTED = 2,   /* a valid size this build has no kernel for */
     KDA_ERR_WORKSPACE = 3,     /* workspace missing or smaller than the query says */
     KDA_ERR_CUDA = 4,          /* a CUDA runtime error while launching */
-    KDA_ERR_TIMEOUT = 5        /* a bounded device-side wait gave up (see kda_last_device_error) */
+    KDA_ERR_TIMEOUT = 5,       /* a bounded device-side wait gave up (see kda_last_device_error) */
+    KDA_ERR_INDEX = 6          /* a length or page number read on the device is out of range (ditto) */
 } kda_status;
 
 typedef enum { KDA_IO_F32 = 0, KDA_IO_BF16 = 1 } kda_io_dtype;
@@ -393,6 +394,120 @@ kda_status kda_fused_recurrent_step(const void* q_raw, const void* k_raw, const 
                                     float l2_eps, kda_io_dtype io, void* stream);
 
 /*
+ * The paged key-value cache of the softmax-attention layers
+ * (m.lqnn.cn/news/205170, section "KDA 与 Gated Attention：每 4 层只留 1 层全注意力": one layer of
+ *  every four keeps full attention over all tokens, with a sigmoid output gate; the KDA layers'
+ *  counterparts of these calls are kda_recurrent_step and its conv cache.)
+ *
+ * Shared by kda_cache_append, kda_paged_decode and kda_cache_evict:
+ *  k_cache, v_cache : pages of page_size slots; element c of head h of slot s of page p is at
+ *                  p*page_stride + s*slot_stride + h*head_stride + c (strides in elements, >= d
+ *                  and a multiple of 16 bytes, the same for both), io dtype. Token-major
+ *                  [pages, page_size, Hkv, d] and head-major [pages, Hkv, page_size, d] arrays
+ *                  are both served. Keys come as the layer attends to them (normalised, rotated).
+ *  block_table   : [N, max_pages] int32: slot s of sequence n lies in page
+ *                  block_table[n, s / page_size]. Entries behind a sequence's length are not read.
+ *  seqlens       : [N] int32, slots in use, before the call. Read on the device, so a captured
+ *                  graph follows them.
+ *  acc           : [N, Hkv, slots] fp32, the attention weight each entry has gathered
+ *  pos           : [N, Hkv, slots] int32, the position in the sequence of each entry's token
+ *  positions     : [N] int32, tokens each sequence has seen (more than seqlens once entries were
+ *                  evicted), or NULL: the same as seqlens
+ *  Lengths and page numbers are checked on the device: a length outside its range is clamped, and
+ *  a slot whose page number is not in [0, num_pages) is left out (not attended to, not written);
+ *  either sets the device error word, and kda_last_device_error then returns KDA_ERR_INDEX.
+ *  Not checked: that no two slots share memory (a page twice in the tables of what one call
+ *  writes), and finite inputs.
+ *  Supported: d in {64, 128}, io F32 or BF16, any page_size.
+ */
+
+/*
+ * kda_cache_append -- writes new tokens' keys and values into the cache.
+ *
+ * Token i of sequence n goes to slot seqlens[n] + i, its acc becomes 0 and its pos becomes
+ * positions[n] + i. seqlens and positions themselves are left as they are.
+ *
+ *  k, v      : [T_tot, Hkv, d] io dtype: padded (B sequences of T tokens; decode is T == 1) or
+ *              packed (cu_seqlens), as for every call
+ *  acc, pos  : as above, or NULL (each on its own)       slots: > 0 with either
+ *  Tokens for which the block table (max_pages pages) or slots leave no room are not written and
+ *  set the error word.
+ */
+kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v_cache,
+                            int64_t page_stride, int64_t slot_stride, int64_t head_stride,
+                            int num_pages, int page_size, const int32_t* block_table,
+                            int max_pages, const int32_t* seqlens, const int32_t* positions,
+                            float* acc, int32_t* pos, int slots, const int32_t* cu_seqlens,
+                            const int32_t* cu_seqlens_host, int B, int T, int N, int Hkv, int d,
+                            kda_io_dtype io, void* stream);
+
+/*
+ * kda_paged_decode_workspace_size -- bytes of device workspace kda_paged_decode needs
+ * (*bytes, host). with_acc: whether acc is given. Host-only. The contents need no initialisation
+ * and are dead after the call: one workspace serves consecutive calls on one stream, and captured
+ * graphs that do not run at the same time.
+ */
+kda_status kda_paged_decode_workspace_size(int N, int Hq, int Hkv, int d, int max_len, int with_acc,
+                                           size_t* bytes);
+
+/*
+ * kda_paged_decode -- attention of one new token per sequence over its paged cache.
+ *
+ * Query head h reads key-value head h / (Hq / Hkv). Over the slots j < seqlens[n]:
+ *     w_j = softmax_j(scale * q . K_j),   o = sum_j w_j V_j,   o *= sigmoid(z) when z is given,
+ *     acc[n, hkv, j] += sum of w_j over the query heads of hkv, when acc is given.
+ * A sequence of length 0 gives o = 0. The new token's own key must be in the cache already
+ * (kda_cache_append). Scores, softmax statistics and sums are fp32; results do not depend on
+ * anything but the inputs and the device's SM count (no atomics).
+ *
+ *  q, z, o : [N, Hq, d] io dtype (z may be NULL); o must not overlap any input
+ *  acc     : [N, Hkv, slots] fp32, updated in place, or NULL      slots: >= max_len with acc
+ *  max_len : host bound on seqlens, <= max_pages * page_size; longer ones are clamped to it and
+ *            set the error word
+ *  workspace: kda_paged_decode_workspace_size() bytes, 16-byte aligned (KDA_ERR_WORKSPACE)
+ */
+kda_status kda_paged_decode(const void* q, const void* k_cache, const void* v_cache,
+                            int64_t page_stride, int64_t slot_stride, int64_t head_stride,
+                            int num_pages, int page_size, const int32_t* block_table,
+                            int max_pages, const int32_t* seqlens, const void* z, float scale,
+                            float* acc, int slots, void* o, int N, int Hq, int Hkv, int d,
+                            int max_len, kda_io_dtype io, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * kda_cache_evict_workspace_size -- bytes of device workspace kda_cache_evict needs (*bytes,
+ * host). Host-only. Workspace rules as for kda_paged_decode.
+ */
+kda_status kda_cache_evict_workspace_size(int N, int Hkv, int max_len, int keep, size_t* bytes);
+
+/*
+ * kda_cache_evict -- cuts every (sequence, head) of the cache to at most keep entries, by the
+ * attention weight that they have gathered.
+ *
+ * Of a sequence longer than keep, each head keeps on its own: first the guarded entries
+ * (pos < n_first or pos >= positions[n] - n_recent), then those of larger acc, of equal ones
+ * those of lower slots (-0 equals 0; NaN ranks below everything). Kept entries in slots < keep stay where
+ * they are; the others, in the order of their slots, move into the free slots < keep, in order:
+ * their K and V rows in place, their acc and pos to acc_out and pos_out. Softmax attention does
+ * not depend on the order of its entries. seqlens_out[n] = min(seqlens[n], keep); the pages
+ * behind it are the caller's again. Shorter sequences keep everything.
+ *
+ *  keep >= 0; n_first, n_recent >= 0 with n_first + n_recent <= keep
+ *  acc, pos : [N, Hkv, slots]           acc_out, pos_out: the same shape, either equal to acc and
+ *             pos (in place) or disjoint from them; slots >= seqlens_out[n] are not written
+ *  seqlens_out : [N] int32, may equal seqlens          max_len: as for kda_paged_decode; <= slots
+ *  A page must not be reached by two sequences of the call (its rows move in place).
+ *  workspace: kda_cache_evict_workspace_size() bytes, 16-byte aligned (KDA_ERR_WORKSPACE)
+ */
+kda_status kda_cache_evict(void* k_cache, void* v_cache, int64_t page_stride, int64_t slot_stride,
+                           int64_t head_stride, int num_pages, int page_size,
+                           const int32_t* block_table, int max_pages, const int32_t* seqlens,
+                           const int32_t* positions, int keep, int n_first, int n_recent,
+                           const float* acc, const int32_t* pos, float* acc_out, int32_t* pos_out,
+                           int slots, int32_t* seqlens_out, int N, int Hkv, int d, int max_len,
+                           kda_io_dtype io, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * kda_set_wait_limit -- bound, in SM clock cycles, of every device-side wait of the prefill
  * kernels launched after this call on any device (0 restores the default of ~2 s). A wait that
  * runs out sets the device error word (KDA_ERR_TIMEOUT from kda_last_device_error) and the
@@ -405,8 +520,9 @@ kda_status kda_set_wait_limit(int64_t cycles);
 /*
  * kda_last_device_error -- synchronises `stream`, then returns and clears the
  * device-side error word that kernels set when a bounded wait gives up
- * (KDA_ERR_TIMEOUT) -- KDA_OK if none. Returns KDA_ERR_CUDA if the stream
- * reports a CUDA error.
+ * (KDA_ERR_TIMEOUT) or an index is out of range (KDA_ERR_INDEX) -- KDA_OK if
+ * none, KDA_ERR_TIMEOUT if both. Returns KDA_ERR_CUDA if the stream reports a
+ * CUDA error.
  */
 kda_status kda_last_device_error(void* stream);
 

@@ -7,10 +7,13 @@
 
 #include <stdint.h>
 
+#include <initializer_list>
+
 #define KDA_API extern "C" __attribute__((visibility("default")))
 
 #include "common.cuh"
 #include "launchers.h"
+#include "paged.cuh"
 
 namespace kda {
 __device__ unsigned int g_device_error = 0;
@@ -106,6 +109,38 @@ int auto_split(int64_t longest, int64_t T_tot, int H, int64_t units, int cluster
     return 10 * best < 9 * unsplit ? best_p : 1;
 }
 
+// The arguments that the calls on the paged cache share.
+kda_status fill_cache(kda::PagedCache* c, const void* k_cache, const void* v_cache,
+                      int64_t page_stride, int64_t slot_stride, int64_t head_stride, int num_pages,
+                      int page_size, const int32_t* block_table, int max_pages, int N, int Hkv,
+                      int d, kda_io_dtype io) {
+    if (io != KDA_IO_F32 && io != KDA_IO_BF16) return KDA_ERR_INVALID_ARG;
+    if (N < 0 || Hkv <= 0 || d <= 0 || page_size <= 0 || num_pages < 0 || max_pages < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (!ok_req(k_cache) || !ok_req(v_cache) || block_table == nullptr || !aligned4(block_table))
+        return KDA_ERR_INVALID_ARG;
+    const int64_t per16 = io == KDA_IO_BF16 ? 8 : 4;          // elements of 16 bytes
+    for (int64_t s : {page_stride, slot_stride, head_stride})
+        if (s < d || s % per16 != 0) return KDA_ERR_INVALID_ARG;
+    // N Hkv counts blocks, and slots are int32
+    if ((int64_t)N * Hkv > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    if (!head_dim_ok(d)) return KDA_ERR_UNSUPPORTED;
+    c->k = const_cast<void*>(k_cache);
+    c->v = const_cast<void*>(v_cache);
+    c->page_stride = page_stride; c->slot_stride = slot_stride; c->head_stride = head_stride;
+    c->num_pages = num_pages; c->page_size = page_size;
+    c->block_table = block_table; c->max_pages = max_pages;
+    c->err = nullptr;
+    return KDA_OK;
+}
+
+// Whether [a, a + n) and [b, b + n) overlap without being the same.
+bool partly_overlaps(const void* a, const void* b, size_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x != y && x < y + n && y < x + n;
+}
+
 }  // namespace
 
 KDA_API const char* kda_status_string(kda_status status) {
@@ -116,6 +151,7 @@ KDA_API const char* kda_status_string(kda_status status) {
         case KDA_ERR_WORKSPACE: return "workspace missing or too small";
         case KDA_ERR_CUDA: return "CUDA error";
         case KDA_ERR_TIMEOUT: return "a bounded device wait timed out";
+        case KDA_ERR_INDEX: return "a length or page number on the device is out of range";
     }
     return "unknown status";
 }
@@ -540,6 +576,135 @@ KDA_API kda_status kda_fused_recurrent_step(
     return from_cuda(kda::launch_recurrent_step(a, static_cast<cudaStream_t>(stream)));
 }
 
+KDA_API kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v_cache,
+                                    int64_t page_stride, int64_t slot_stride, int64_t head_stride,
+                                    int num_pages, int page_size, const int32_t* block_table,
+                                    int max_pages, const int32_t* seqlens, const int32_t* positions,
+                                    float* acc, int32_t* pos, int slots, const int32_t* cu_seqlens,
+                                    const int32_t* cu_seqlens_host, int B, int T, int N, int Hkv,
+                                    int d, kda_io_dtype io, void* stream) {
+    int64_t T_tot = 0;
+    int Nn = 0;
+    if (!batch_geometry(cu_seqlens, cu_seqlens_host, B, T, N, &T_tot, &Nn)) return KDA_ERR_INVALID_ARG;
+    kda::AppendArgs a;
+    const kda_status st = fill_cache(&a.c, k_cache, v_cache, page_stride, slot_stride, head_stride,
+                                     num_pages, page_size, block_table, max_pages, Nn, Hkv, d, io);
+    if (st != KDA_OK && st != KDA_ERR_UNSUPPORTED) return st;
+    if (!ok_req(k) || !ok_req(v) || seqlens == nullptr || !aligned4(seqlens) || !aligned4(positions) ||
+        !aligned4(acc) || !aligned4(pos) || !aligned4(cu_seqlens))
+        return KDA_ERR_INVALID_ARG;
+    if (slots < 0 || ((acc != nullptr || pos != nullptr) && slots == 0)) return KDA_ERR_INVALID_ARG;
+    if (st != KDA_OK || T_tot > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    a.c.err = device_error_word();
+    if (a.c.err == nullptr) return KDA_ERR_CUDA;
+    a.k = k; a.v = v;
+    a.seqlens = seqlens;
+    a.positions = positions ? positions : seqlens;
+    a.acc = acc; a.pos = pos; a.slots = slots;
+    a.cu = cu_seqlens;
+    a.T_tot = T_tot;
+    a.T_pad = cu_seqlens ? 0 : T;
+    a.N = Nn; a.H = Hkv; a.d = d;
+    a.io = io == KDA_IO_BF16 ? kda::Io::BF16 : kda::Io::F32;
+    return from_cuda(kda::launch_cache_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+KDA_API kda_status kda_paged_decode_workspace_size(int N, int Hq, int Hkv, int d, int max_len,
+                                                   int with_acc, size_t* bytes) {
+    if (bytes == nullptr || N < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || d <= 0 || max_len < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (!kda::paged_decode_workspace(N, Hq, Hkv, d, max_len, with_acc != 0, bytes))
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+KDA_API kda_status kda_paged_decode(const void* q, const void* k_cache, const void* v_cache,
+                                    int64_t page_stride, int64_t slot_stride, int64_t head_stride,
+                                    int num_pages, int page_size, const int32_t* block_table,
+                                    int max_pages, const int32_t* seqlens, const void* z,
+                                    float scale, float* acc, int slots, void* o, int N, int Hq,
+                                    int Hkv, int d, int max_len, kda_io_dtype io, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    kda::DecodeArgs a;
+    const kda_status st = fill_cache(&a.c, k_cache, v_cache, page_stride, slot_stride, head_stride,
+                                     num_pages, page_size, block_table, max_pages, N, Hkv, d, io);
+    if (st != KDA_OK && st != KDA_ERR_UNSUPPORTED) return st;
+    if (Hq <= 0 || Hq % Hkv != 0 || !ok_req(q) || !ok_req(o) || !ok_opt(z) || seqlens == nullptr ||
+        !aligned4(seqlens) || !aligned4(acc))
+        return KDA_ERR_INVALID_ARG;
+    if (max_len < 0 || max_len > (int64_t)max_pages * page_size) return KDA_ERR_INVALID_ARG;
+    if (acc != nullptr && (slots <= 0 || slots < max_len)) return KDA_ERR_INVALID_ARG;
+    size_t need = 0;
+    if (st != KDA_OK || (int64_t)N * Hq > INT32_MAX ||
+        !kda::paged_decode_workspace(N, Hq, Hkv, d, max_len, acc != nullptr, &need))
+        return KDA_ERR_UNSUPPORTED;
+    if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
+        return KDA_ERR_WORKSPACE;
+    a.c.err = device_error_word();
+    if (a.c.err == nullptr) return KDA_ERR_CUDA;
+    a.q = q; a.z = z;
+    a.seqlens = seqlens;
+    a.scale = scale;
+    a.acc = acc; a.slots = slots;
+    a.o = o;
+    a.N = N; a.Hq = Hq; a.H = Hkv; a.d = d;
+    a.max_len = max_len;
+    a.io = io == KDA_IO_BF16 ? kda::Io::BF16 : kda::Io::F32;
+    a.workspace = workspace;
+    return from_cuda(kda::launch_paged_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+KDA_API kda_status kda_cache_evict_workspace_size(int N, int Hkv, int max_len, int keep,
+                                                  size_t* bytes) {
+    if (bytes == nullptr || N < 0 || Hkv <= 0 || max_len < 0 || keep < 0) return KDA_ERR_INVALID_ARG;
+    if (!kda::cache_evict_workspace(N, Hkv, max_len, keep, bytes)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+KDA_API kda_status kda_cache_evict(void* k_cache, void* v_cache, int64_t page_stride,
+                                   int64_t slot_stride, int64_t head_stride, int num_pages,
+                                   int page_size, const int32_t* block_table, int max_pages,
+                                   const int32_t* seqlens, const int32_t* positions, int keep,
+                                   int n_first, int n_recent, const float* acc, const int32_t* pos,
+                                   float* acc_out, int32_t* pos_out, int slots,
+                                   int32_t* seqlens_out, int N, int Hkv, int d, int max_len,
+                                   kda_io_dtype io, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    kda::EvictArgs a;
+    const kda_status st = fill_cache(&a.c, k_cache, v_cache, page_stride, slot_stride, head_stride,
+                                     num_pages, page_size, block_table, max_pages, N, Hkv, d, io);
+    if (st != KDA_OK && st != KDA_ERR_UNSUPPORTED) return st;
+    const void* req[] = {seqlens, acc, pos, acc_out, pos_out, seqlens_out};
+    for (const void* p : req)
+        if (p == nullptr || !aligned4(p)) return KDA_ERR_INVALID_ARG;
+    if (!aligned4(positions)) return KDA_ERR_INVALID_ARG;
+    if (keep < 0 || n_first < 0 || n_recent < 0 || (int64_t)n_first + n_recent > keep)
+        return KDA_ERR_INVALID_ARG;
+    if (max_len < 0 || max_len > (int64_t)max_pages * page_size || slots < max_len)
+        return KDA_ERR_INVALID_ARG;
+    const size_t side = (size_t)N * Hkv * (size_t)slots * 4;
+    if (partly_overlaps(acc, acc_out, side) || partly_overlaps(pos, pos_out, side))
+        return KDA_ERR_INVALID_ARG;
+    size_t need = 0;
+    if (st != KDA_OK || !kda::cache_evict_workspace(N, Hkv, max_len, keep, &need))
+        return KDA_ERR_UNSUPPORTED;
+    if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
+        return KDA_ERR_WORKSPACE;
+    a.c.err = device_error_word();
+    if (a.c.err == nullptr) return KDA_ERR_CUDA;
+    a.seqlens = seqlens;
+    a.positions = positions ? positions : seqlens;
+    a.keep = keep; a.n_first = n_first; a.n_recent = n_recent;
+    a.acc = acc; a.pos = pos; a.acc_out = acc_out; a.pos_out = pos_out;
+    a.slots = slots;
+    a.seqlens_out = seqlens_out;
+    a.N = N; a.H = Hkv; a.d = d;
+    a.max_len = max_len;
+    a.io = io == KDA_IO_BF16 ? kda::Io::BF16 : kda::Io::F32;
+    a.workspace = workspace;
+    return from_cuda(kda::launch_cache_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
 KDA_API kda_status kda_set_wait_limit(int64_t cycles) {
     if (cycles < 0) return KDA_ERR_INVALID_ARG;
     kda::g_chunk_wait_cycles = cycles;
@@ -556,7 +721,7 @@ KDA_API kda_status kda_last_device_error(void* stream) {
         const unsigned int zero = 0;
         if (cudaMemcpyToSymbol(kda::g_device_error, &zero, sizeof(zero)) != cudaSuccess)
             return KDA_ERR_CUDA;
-        return KDA_ERR_TIMEOUT;
+        return (word & kda::kErrTimeout) ? KDA_ERR_TIMEOUT : KDA_ERR_INDEX;
     }
     return KDA_OK;
 }

@@ -143,4 +143,66 @@ struct CorrectArgs {
 };
 cudaError_t launch_stretch_correct(const CorrectArgs& a, cudaStream_t stream);
 
+// The paged key-value cache: pages of page_size slots, element strides shared by K and V.
+struct PagedCache {
+    void *k, *v;
+    int64_t page_stride, slot_stride, head_stride;
+    int num_pages, page_size;
+    const int32_t* block_table;      // [N, max_pages]
+    int max_pages;
+    unsigned int* err;               // device error word (kErrIndex)
+};
+
+struct AppendArgs {
+    PagedCache c;
+    const void *k, *v;               // [T_tot, H, d]
+    const int32_t* seqlens;
+    const int32_t* positions;        // or null: seqlens
+    float* acc;                      // [N, H, slots] or null
+    int32_t* pos;                    // [N, H, slots] or null
+    int slots;
+    const int32_t* cu;               // device cu_seqlens or null (padded)
+    int64_t T_tot;
+    int T_pad;
+    int N, H, d;
+    Io io;
+};
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
+
+struct DecodeArgs {
+    PagedCache c;
+    const void *q, *z;               // [N, Hq, d]; z may be null
+    const int32_t* seqlens;
+    float scale;
+    float* acc;                      // [N, H, slots] or null
+    int slots;
+    void* o;
+    int N, Hq, H, d;                 // H: key-value heads
+    int max_len;
+    Io io;
+    void* workspace;
+};
+// Workspace of launch_paged_decode; false if the size overflows.
+bool paged_decode_workspace(int64_t N, int64_t Hq, int64_t H, int d, int64_t max_len, bool with_acc,
+                            size_t* bytes);
+cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t stream);
+
+struct EvictArgs {
+    PagedCache c;
+    const int32_t *seqlens, *positions;
+    int keep, n_first, n_recent;
+    const float* acc;
+    const int32_t* pos;
+    float* acc_out;
+    int32_t* pos_out;
+    int slots;
+    int32_t* seqlens_out;
+    int N, H, d;
+    int max_len;
+    Io io;
+    void* workspace;
+};
+bool cache_evict_workspace(int64_t N, int64_t H, int64_t max_len, int64_t keep, size_t* bytes);
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream);
+
 }  // namespace kda

@@ -1,0 +1,32 @@
+// paged.cuh -- device helpers of the calls on the paged key-value cache.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+#include "launchers.h"
+
+namespace kda {
+
+// Bit of the device error word: a length or page number read on the device is out of range.
+constexpr unsigned int kErrIndex = 2u;
+
+// A length read on the device, clamped to [0, most].
+__device__ __forceinline__ int checked_len(int len, int most, unsigned int* err) {
+    if (len >= 0 && len <= most) return len;
+    atomicOr(err, kErrIndex);
+    return len < 0 ? 0 : most;
+}
+
+// Element offset of (slot, head 0) of sequence n in the K and V pages, -1 when the page number is
+// out of range. The slot must be below max_pages * page_size.
+__device__ __forceinline__ int64_t slot_offset(const PagedCache& c, int64_t n, int slot) {
+    const int page = __ldg(c.block_table + n * c.max_pages + slot / c.page_size);
+    if (page < 0 || page >= c.num_pages) {
+        atomicOr(c.err, kErrIndex);
+        return -1;
+    }
+    return page * c.page_stride + (slot % c.page_size) * c.slot_stride;
+}
+
+}  // namespace kda

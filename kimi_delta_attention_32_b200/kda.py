@@ -17,7 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libkda.so")
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE, KDA_ERR_CUDA, \
-    KDA_ERR_TIMEOUT = range(6)
+    KDA_ERR_TIMEOUT, KDA_ERR_INDEX = range(7)
 KDA_IO_F32, KDA_IO_BF16 = 0, 1
 
 EXPORTED = ("kda_status_string", "kda_version", "kda_conv_fwd", "kda_chunk_fwd_workspace_size",
@@ -25,7 +25,8 @@ EXPORTED = ("kda_status_string", "kda_version", "kda_conv_fwd", "kda_chunk_fwd_w
             "kda_conv_recurrent_step", "kda_fused_recurrent_step", "kda_set_wait_limit",
             "kda_last_device_error", "kda_chunk_states", "kda_state_scan",
             "kda_chunk_fwd_split_workspace_size", "kda_chunk_fwd_split", "kda_output_correct",
-            "kda_chunk_fwd_split_plan")
+            "kda_chunk_fwd_split_plan", "kda_cache_append", "kda_paged_decode_workspace_size",
+            "kda_paged_decode", "kda_cache_evict_workspace_size", "kda_cache_evict")
 
 _lock = threading.Lock()
 _lib = None
@@ -103,6 +104,21 @@ def load_library(path: str = LIB_PATH):
         lib.kda_chunk_fwd_split_plan.argtypes = [cip, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci,
                                                  ctypes.POINTER(ci), ctypes.POINTER(cs)]
         lib.kda_chunk_fwd_split_plan.restype = ci
+        c64 = ctypes.c_int64
+        lib.kda_cache_append.argtypes = [vp, vp, vp, vp, c64, c64, c64, ci, ci, i32p, ci, i32p, i32p,
+                                         fp, i32p, ci, i32p, cip, ci, ci, ci, ci, ci, ci, vp]
+        lib.kda_cache_append.restype = ci
+        lib.kda_paged_decode_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci, ctypes.POINTER(cs)]
+        lib.kda_paged_decode_workspace_size.restype = ci
+        lib.kda_paged_decode.argtypes = [vp, vp, vp, c64, c64, c64, ci, ci, i32p, ci, i32p, vp, cf,
+                                         fp, ci, vp, ci, ci, ci, ci, ci, ci, vp, cs, vp]
+        lib.kda_paged_decode.restype = ci
+        lib.kda_cache_evict_workspace_size.argtypes = [ci, ci, ci, ci, ctypes.POINTER(cs)]
+        lib.kda_cache_evict_workspace_size.restype = ci
+        lib.kda_cache_evict.argtypes = [vp, vp, c64, c64, c64, ci, ci, i32p, ci, i32p, i32p, ci, ci,
+                                        ci, fp, i32p, fp, i32p, ci, i32p, ci, ci, ci, ci, ci, vp, cs,
+                                        vp]
+        lib.kda_cache_evict.restype = ci
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -413,6 +429,202 @@ def fused_recurrent_step(q_raw, k_raw, v_raw, g_raw, beta_raw, w_q, w_k, w_v, co
                                       _stream(stream))
     _check("kda_fused_recurrent_step", st)
     return o
+
+
+def _need(name, t, dtype, shape, device, none_ok=False):
+    """t is a dense tensor of this dtype and shape on this device (or None where that is allowed)."""
+    if t is None:
+        if none_ok:
+            return
+        raise TypeError(f"{name} is required")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+
+
+def _paged(k_cache, v_cache, block_table, seqlens):
+    """Checks the cache tensors; returns (C arguments up to max_pages, N, page_size, Hkv, d)."""
+    _io(k_cache)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or \
+            k_cache.device != v_cache.device or block_table.dim() != 2:
+        raise ValueError("k_cache and v_cache: two [pages, page_size, Hkv, d] tensors of one dtype "
+                         "and device; block_table: [N, max_pages]")
+    dev = k_cache.device
+    pages, page_size, H, d = k_cache.shape
+    # strides; that of a dimension of size 1 is never used
+    sk, sv = ([st if n > 1 else d for n, st in zip(t.shape[:3], t.stride())]
+              for t in (k_cache, v_cache))
+    if sk != sv or (d > 1 and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1)):
+        raise ValueError("k_cache and v_cache need the same strides, with the last dimension dense")
+    N, max_pages = block_table.shape
+    _need("block_table", block_table, torch.int32, (N, max_pages), dev)
+    _need("seqlens", seqlens, torch.int32, (N,), dev)
+    return (_ptr(k_cache), _ptr(v_cache), *sk, pages, page_size, _ptr(block_table),
+            max_pages), N, page_size, H, d
+
+
+def _call_on(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    if device.type != "cuda":
+        raise ValueError(f"the cache must be a CUDA tensor, not {device}")
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def cache_append(k, v, k_cache, v_cache, block_table, seqlens, positions=None, acc=None, pos=None,
+                 cu_seqlens=None, cu_host=None, stream=None):
+    """Writes new tokens into the paged cache: token i of sequence n to slot seqlens[n] + i.
+    Packed: k, v [T_tot,Hkv,d] with cu_seqlens (device int32) and cu_host (list); padded:
+    [B,T,Hkv,d] (decode: T = 1). k_cache, v_cache [pages,page_size,Hkv,d] with any strides (d
+    dense); block_table [N,max_pages], seqlens and positions [N], int32; acc (fp32) and pos
+    (int32) [N,Hkv,slots], whose new entries become 0 and positions[n] + i (seqlens[n] + i without
+    positions). seqlens and positions are not advanced."""
+    lib = load_library()
+    cache, N, _, H, d = _paged(k_cache, v_cache, block_table, seqlens)
+    dev = k_cache.device
+    if cu_seqlens is None:
+        if k.dim() != 4:
+            raise ValueError("without cu_seqlens k is [B, T, Hkv, d]")
+        B, T = k.shape[:2]
+        if B != N:
+            raise ValueError(f"k has {B} sequences, block_table {N}")
+        shape = (B, T, H, d)
+    else:
+        B, T = 1, 0
+        _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
+        if cu_host is None or len(cu_host) != N + 1:
+            raise ValueError("cu_host must hold the values of cu_seqlens")
+        shape = (int(cu_host[N]), H, d)
+    _need("k", k, k_cache.dtype, shape, dev)
+    _need("v", v, k_cache.dtype, shape, dev)
+    _need("positions", positions, torch.int32, (N,), dev, none_ok=True)
+    side = acc if acc is not None else pos
+    slots = 0
+    if side is not None:
+        slots = side.shape[-1]
+        _need("acc", acc, torch.float32, (N, H, slots), dev, none_ok=True)
+        _need("pos", pos, torch.int32, (N, H, slots), dev, none_ok=True)
+        if slots == 0 and k.numel():
+            raise ValueError("acc and pos have no slots")
+    if k.numel() == 0:
+        return
+    keep, cuh = _host_cu(cu_host if cu_seqlens is not None else None)
+    st = _call_on(dev, stream, lib.kda_cache_append, _ptr(k), _ptr(v), *cache, _ptr(seqlens),
+                  _ptr(positions), _ptr(acc), _ptr(pos), slots, _ptr(cu_seqlens), cuh, B, T, N, H,
+                  d, _io(k_cache))
+    del keep
+    _check("kda_cache_append", st)
+
+
+def paged_decode_workspace_size(N, Hq, Hkv, d, max_len, with_acc=False) -> int:
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    _check("kda_paged_decode_workspace_size",
+           lib.kda_paged_decode_workspace_size(N, Hq, Hkv, d, max_len, int(with_acc),
+                                               ctypes.byref(out)))
+    return out.value
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace: a contiguous uint8 tensor on the cache's device")
+    return workspace
+
+
+def paged_decode(q, k_cache, v_cache, block_table, seqlens, scale=1.0, z=None, acc=None,
+                 max_len=None, o=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over its paged cache: q [N,Hq,d] over the slots
+    below seqlens [N] of the cache (as for cache_append), softmax(scale q K^T) V, times
+    sigmoid(z) when z [N,Hq,d] is given. acc [N,Hkv,slots] fp32 gathers the weights, summed over
+    the query heads of each key-value head. max_len: host bound on seqlens (default: what
+    block_table can hold, or acc's slots). Returns o [N,Hq,d]."""
+    lib = load_library()
+    cache, N, page_size, H, d = _paged(k_cache, v_cache, block_table, seqlens)
+    dev = k_cache.device
+    if q.dim() != 3:
+        raise ValueError("q is [N, Hq, d]")
+    Hq = q.shape[1]
+    _need("q", q, k_cache.dtype, (N, Hq, d), dev)
+    _need("z", z, k_cache.dtype, (N, Hq, d), dev, none_ok=True)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _need("o", o, k_cache.dtype, (N, Hq, d), dev)
+    slots = 0
+    if acc is not None:
+        slots = acc.shape[-1]
+        _need("acc", acc, torch.float32, (N, H, slots), dev)
+    if N == 0:
+        return o
+    if max_len is None:
+        max_len = block_table.shape[1] * page_size
+        if acc is not None:
+            max_len = min(max_len, slots)
+    if workspace is None:
+        workspace = _workspace(None, paged_decode_workspace_size(N, Hq, H, d, max_len,
+                                                                 acc is not None), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    st = _call_on(dev, stream, lib.kda_paged_decode, _ptr(q), *cache, _ptr(seqlens), _ptr(z),
+                  float(scale), _ptr(acc), slots, _ptr(o), N, Hq, H, d, max_len, _io(q),
+                  _ptr(workspace), 0 if workspace is None else workspace.numel())
+    _check("kda_paged_decode", st)
+    return o
+
+
+def cache_evict_workspace_size(N, Hkv, max_len, keep) -> int:
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    _check("kda_cache_evict_workspace_size",
+           lib.kda_cache_evict_workspace_size(N, Hkv, max_len, keep, ctypes.byref(out)))
+    return out.value
+
+
+def cache_evict(k_cache, v_cache, block_table, seqlens, keep, acc, pos, positions=None, n_first=0,
+                n_recent=0, acc_out=None, pos_out=None, seqlens_out=None, max_len=None,
+                workspace=None, stream=None):
+    """Cuts every (sequence, head) of the paged cache to its keep entries of largest acc; entries
+    with pos < n_first or pos >= positions[n] - n_recent stay before all others. Kept entries
+    behind slot keep move into the slots that became free (K and V in place; acc and pos into
+    acc_out and pos_out, by default in place too). Returns the new lengths (seqlens_out)."""
+    lib = load_library()
+    cache, N, page_size, H, d = _paged(k_cache, v_cache, block_table, seqlens)
+    dev = k_cache.device
+    _need("acc", acc, torch.float32, (N, H, acc.shape[-1]), dev)
+    slots = acc.shape[-1]
+    _need("pos", pos, torch.int32, (N, H, slots), dev)
+    _need("positions", positions, torch.int32, (N,), dev, none_ok=True)
+    acc_out = acc if acc_out is None else acc_out
+    pos_out = pos if pos_out is None else pos_out
+    _need("acc_out", acc_out, torch.float32, (N, H, slots), dev)
+    _need("pos_out", pos_out, torch.int32, (N, H, slots), dev)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens)
+    else:
+        _need("seqlens_out", seqlens_out, torch.int32, (N,), dev)
+    if N == 0:
+        return seqlens_out
+    if max_len is None:
+        max_len = min(block_table.shape[1] * page_size, slots)
+    if workspace is None:
+        workspace = _workspace(None, cache_evict_workspace_size(N, H, max_len, keep), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    st = _call_on(dev, stream, lib.kda_cache_evict, *cache, _ptr(seqlens), _ptr(positions), keep,
+                  n_first, n_recent, _ptr(acc), _ptr(pos), _ptr(acc_out), _ptr(pos_out), slots,
+                  _ptr(seqlens_out), N, H, d, max_len, _io(k_cache), _ptr(workspace),
+                  0 if workspace is None else workspace.numel())
+    _check("kda_cache_evict", st)
+    return seqlens_out
 
 
 def set_wait_limit(cycles: int) -> None:

@@ -1,0 +1,201 @@
+"""CPU tests of the paged cache's entry points: the C ABI's and the binding's refusals, and the
+workspace queries."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+from kimi_delta_attention_32_b200 import build as kbuild
+from kimi_delta_attention_32_b200 import kda
+from test_abi import FAKE, MIS, _cu_host
+
+INV, UNS, WS = kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED, kda.KDA_ERR_WORKSPACE
+ODD = ctypes.c_void_p(0x10002)           # not even 4-byte aligned
+
+
+@pytest.fixture(scope="module")
+def lib():
+    kbuild.build()
+    return kda.load_library()
+
+
+CACHE = dict(kc=FAKE, vc=FAKE, ps=16 * 2 * 128, ss=2 * 128, hs=128, np=8, page=16, bt=FAKE, mp=4)
+
+
+def _append(lib, **kw):
+    a = dict(CACHE, k=FAKE, v=FAKE, sl=FAKE, po=None, acc=None, pos=None, slots=0, cu=None, cuh=None,
+             B=2, T=1, N=0, H=2, d=128, io=1)
+    a.update(kw)
+    return lib.kda_cache_append(a["k"], a["v"], a["kc"], a["vc"], a["ps"], a["ss"], a["hs"], a["np"],
+                                a["page"], a["bt"], a["mp"], a["sl"], a["po"], a["acc"], a["pos"],
+                                a["slots"], a["cu"], a["cuh"], a["B"], a["T"], a["N"], a["H"],
+                                a["d"], a["io"], None)
+
+
+def _decode(lib, **kw):
+    a = dict(CACHE, q=FAKE, sl=FAKE, z=None, scale=1.0, acc=None, slots=0, o=FAKE, N=2, Hq=8, H=2,
+             d=128, ml=64, io=1, ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return lib.kda_paged_decode(a["q"], a["kc"], a["vc"], a["ps"], a["ss"], a["hs"], a["np"],
+                                a["page"], a["bt"], a["mp"], a["sl"], a["z"], a["scale"], a["acc"],
+                                a["slots"], a["o"], a["N"], a["Hq"], a["H"], a["d"], a["ml"],
+                                a["io"], a["ws"], a["wsb"], None)
+
+
+def _evict(lib, **kw):
+    a = dict(CACHE, sl=FAKE, po=None, keep=32, nf=4, nr=8, acc=FAKE, pos=FAKE, ao=FAKE, qo=FAKE,
+             slots=64, so=FAKE, N=2, H=2, d=128, ml=64, io=1, ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return lib.kda_cache_evict(a["kc"], a["vc"], a["ps"], a["ss"], a["hs"], a["np"], a["page"],
+                               a["bt"], a["mp"], a["sl"], a["po"], a["keep"], a["nf"], a["nr"],
+                               a["acc"], a["pos"], a["ao"], a["qo"], a["slots"], a["so"], a["N"],
+                               a["H"], a["d"], a["ml"], a["io"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("fn", [_append, _decode, _evict])
+@pytest.mark.parametrize("kw,status", [
+    (dict(kc=None), INV), (dict(vc=MIS), INV), (dict(bt=None), INV), (dict(bt=ODD), INV),
+    (dict(sl=None), INV), (dict(sl=ODD), INV), (dict(page=0), INV), (dict(np=-1), INV),
+    (dict(mp=-1), INV), (dict(H=0), INV), (dict(d=0), INV), (dict(io=7), INV),
+    (dict(ps=0), INV), (dict(ss=-256), INV), (dict(hs=64), INV),       # strides below d
+    (dict(hs=129), INV),                                               # not 16 bytes
+    (dict(io=0, ss=258), INV),
+    (dict(d=96, hs=96), UNS), (dict(d=32), UNS), (dict(mp=1 << 30), UNS),
+])
+def test_cache_arguments_are_checked(lib, fn, kw, status):
+    assert fn(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=None), INV), (dict(v=MIS), INV), (dict(po=ODD), INV), (dict(acc=FAKE), INV),
+    (dict(pos=FAKE, slots=0), INV), (dict(slots=-1), INV), (dict(acc=ODD, slots=8), INV),
+    (dict(B=-1), INV), (dict(B=1 << 16, T=1 << 16), UNS), (dict(cu=FAKE), INV),
+])
+def test_append_refuses(lib, kw, status):
+    assert _append(lib, **kw) == status
+
+
+def test_append_refuses_bad_cu_seqlens(lib):
+    keep, cuh = _cu_host([0, 3, 2])
+    assert _append(lib, cu=FAKE, cuh=cuh, N=2) == INV
+    keep2, cuh = _cu_host([1, 2, 3])
+    assert _append(lib, cu=FAKE, cuh=cuh, N=2) == INV
+    del keep, keep2
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INV), (dict(o=MIS), INV), (dict(z=MIS), INV), (dict(Hq=7), INV), (dict(Hq=0), INV),
+    (dict(N=-1), INV), (dict(ml=-1), INV), (dict(ml=65), INV),         # beyond the block table
+    (dict(acc=FAKE), INV), (dict(acc=FAKE, slots=63), INV), (dict(acc=ODD, slots=64), INV),
+    (dict(ws=None), WS), (dict(ws=MIS), WS),
+    (dict(N=1 << 15, H=1, Hq=1 << 17), UNS),                           # N * Hq counts blocks
+])
+def test_decode_refuses(lib, kw, status):
+    assert _decode(lib, **kw) == status
+
+
+def test_decode_refuses_a_short_workspace(lib):
+    out = ctypes.c_size_t(0)
+    for with_acc in (0, 1):
+        assert lib.kda_paged_decode_workspace_size(2, 8, 2, 128, 64, with_acc, ctypes.byref(out)) == 0
+        kw = dict(acc=FAKE, slots=64) if with_acc else {}
+        assert _decode(lib, wsb=out.value - 1, **kw) == WS
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(acc=None), INV), (dict(pos=None), INV), (dict(ao=None), INV), (dict(qo=None), INV),
+    (dict(so=None), INV), (dict(so=ODD), INV), (dict(po=ODD), INV),
+    (dict(keep=-1), INV), (dict(nf=-1), INV), (dict(nr=-1), INV), (dict(nf=25, nr=8), INV),
+    (dict(nf=2 ** 31 - 1, nr=2 ** 31 - 1), INV),
+    (dict(ml=65, slots=100), INV), (dict(ml=64, slots=63), INV), (dict(ml=-1), INV),
+    (dict(ao=ctypes.c_void_p(0x10000 + 64)), INV),                     # overlaps acc in part
+    (dict(qo=ctypes.c_void_p(0x10000 - 64)), INV),
+    (dict(ws=MIS), WS), (dict(wsb=3), WS),
+])
+def test_evict_refuses(lib, kw, status):
+    assert _evict(lib, **kw) == status
+
+
+def test_workspace_queries(lib):
+    out = ctypes.c_size_t(0)
+    size = lib.kda_paged_decode_workspace_size
+    assert size(4, 32, 8, 128, 1000, 0, None) == INV
+    assert size(4, 32, 7, 128, 1000, 0, ctypes.byref(out)) == INV
+    assert size(-1, 32, 8, 128, 1000, 0, ctypes.byref(out)) == INV
+    assert size(4, 32, 8, 128, -1, 0, ctypes.byref(out)) == INV
+    assert size(2 ** 30, 2 ** 30, 1, 128, 2 ** 30, 1, ctypes.byref(out)) == UNS    # over 2^63 bytes
+    assert size(4, 32, 8, 128, 1000, 0, ctypes.byref(out)) == 0
+    plain = out.value
+    assert size(4, 32, 8, 128, 1000, 1, ctypes.byref(out)) == 0
+    assert out.value >= plain
+    size = lib.kda_cache_evict_workspace_size
+    assert size(4, 8, 1000, -1, ctypes.byref(out)) == INV
+    assert size(4, 0, 1000, 10, ctypes.byref(out)) == INV
+    assert size(4, 8, 1000, 400, None) == INV
+    assert size(4, 8, 1000, 400, ctypes.byref(out)) == 0
+
+
+def test_index_status_has_a_text(lib):
+    assert kda.KDA_ERR_INDEX == 6 and b"out of range" in lib.kda_status_string(6)
+
+
+def _tensors(io=torch.bfloat16, N=2, H=2, d=128, page=16, pages=8):
+    c = torch.zeros(pages, page, H, d, dtype=io)
+    i32 = dict(dtype=torch.int32)
+    return dict(k_cache=c, v_cache=c.clone(), block_table=torch.zeros(N, 4, **i32),
+                seqlens=torch.zeros(N, **i32))
+
+
+def test_binding_refuses():
+    """The binding's checks come before any call; tensors on the host are refused last."""
+    t = _tensors()
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    ws = torch.zeros(16, dtype=torch.uint8)
+
+    def dec(q=q, **kw):
+        a = dict(t, workspace=ws)
+        a.update(kw)
+        return kda.paged_decode(q, **a)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        dec()
+    with pytest.raises(TypeError):
+        dec(q=q.float())
+    with pytest.raises(ValueError, match="contiguous"):
+        dec(q=torch.zeros(8, 2, 128, dtype=torch.bfloat16).transpose(0, 1))
+    with pytest.raises(ValueError, match="shape"):
+        dec(q=q[:1])
+    with pytest.raises(ValueError, match="shape"):
+        dec(seqlens=t["seqlens"][:1])
+    with pytest.raises(TypeError):
+        dec(block_table=t["block_table"].long())
+    with pytest.raises(ValueError, match="stride"):
+        dec(v_cache=t["v_cache"].transpose(1, 2).contiguous().transpose(1, 2))
+    with pytest.raises(ValueError, match="stride"):
+        dec(k_cache=torch.zeros(8, 16, 2, 256, dtype=torch.bfloat16)[..., ::2],
+            v_cache=torch.zeros(8, 16, 2, 256, dtype=torch.bfloat16)[..., ::2])
+    with pytest.raises(ValueError):
+        dec(v_cache=t["v_cache"][:4])
+    with pytest.raises(TypeError):
+        dec(k_cache=t["k_cache"].half(), v_cache=t["v_cache"].half())
+    with pytest.raises(ValueError, match="workspace"):
+        dec(workspace=torch.zeros(16))
+    with pytest.raises(TypeError):
+        dec(acc=torch.zeros(2, 2, 64, dtype=torch.float64))
+    k = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        kda.cache_append(k, k, **t)
+    with pytest.raises(ValueError, match="sequences"):
+        kda.cache_append(k[:1], k[:1], **t)
+    with pytest.raises(ValueError):
+        kda.cache_append(k[:, 0], k[:, 0], **t)          # packed without cu_seqlens
+    with pytest.raises(ValueError, match="cu_host"):
+        kda.cache_append(k[:, 0], k[:, 0], cu_seqlens=torch.zeros(3, dtype=torch.int32), **t)
+    acc, pos = torch.zeros(2, 2, 64), torch.zeros(2, 2, 64, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        kda.cache_evict(keep=8, acc=acc, pos=pos, workspace=ws, **t)
+    with pytest.raises(ValueError, match="shape"):
+        kda.cache_evict(keep=8, acc=acc, pos=pos[:, :, :32], workspace=ws, **t)
+    with pytest.raises(TypeError, match="required"):
+        kda.cache_evict(keep=8, acc=acc, pos=None, workspace=ws, **t)
