@@ -4,96 +4,750 @@
 //
 // Per (sequence, query head), over the slots j < len:  s_j = scale q . K_j,  w = softmax(s),
 // o = sum_j w_j V_j, o *= sigmoid(z); the weights are added to acc per key-value head.
+//
+// What bounds it: every key and value is read once and meets only the G = Hq / Hkv queries of its
+// head, G flops a byte in bf16, so HBM does. The design is a stream of K and V rows through shared
+// memory that never waits for the arithmetic.
+//
+// Division. A segment is (sequence, key-value head, tile of at most 8 NT query heads). Its slots
+// are cut into tiles of 16 W slots (W warps); all tiles of all segments, in order, are divided
+// evenly over a grid that just fills the GPU (decode_split.h), whatever the mix of lengths. A
+// segment inside one block is finished by it; the parts of a segment that spans blocks are joined
+// by a second kernel. Lengths are read on the device: the grid does not depend on them.
+//
+// One pass, online softmax. Each warp takes 16 slots of a tile and keeps its own running maximum,
+// sum and output in registers, so warps meet only at a segment's end. The slots are the M side of
+// the products and the queries the N side (padded to 8, not 16): S^T = K Q^T and O^T = V^T P^T.
+// With M >= 64 rows an instruction, the tcgen05 path would be at least 7/8 padding for such G and
+// its operands would pass through tensor memory; the warp-level MMA feeds from ldmatrix directly
+// and needs a tenth of the tile's streaming time.
+//  - bf16: m16n8k16, P rounded to bf16 (each weight off by half a step, 2^-9 of it on average:
+//    below the rounding of the output itself); l sums the unrounded weights in fp32.
+//  - fp32: m16n8k8 TF32, each operand split in two (x = hi + lo, both TF32) and three products,
+//    which leaves 3 x 2^-22 of a product: fp32's own size.
+//
+// Memory. Every warp owns a ring of S stages (16 K rows and 16 V rows each), filled by 16-byte
+// cp.async and waited for by its own lanes only. 16-byte piece c of row r lies at piece c ^ (r % 8):
+// ldmatrix reads eight rows without a bank conflict. The row addresses of a tile come from the
+// block table one tile before they are used, so a load never waits for its page number. Rows
+// behind the end or with a bad page number are filled with zeros and masked.
+#include "decode_split.h"
 #include "paged.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kMaxBlocks = 320;          // blocks of one launch: 2 an SM, for up to 160 SMs
+constexpr int kMergeFloats = 2048;       // shared floats for joining a block's warps
 
-__device__ __forceinline__ float block_reduce(float x, bool is_max, float* buf) {
-    for (int o = 16; o > 0; o >>= 1) {
-        const float y = __shfl_xor_sync(0xffffffffu, x, o);
-        x = is_max ? fmaxf(x, y) : x + y;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = buf[0];
-    for (int w = 1; w < kThreads / 32; ++w) x = is_max ? fmaxf(x, buf[w]) : x + buf[w];
-    return x;
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes, or zeros when !live (src is then not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo up to 2^-22 x, both TF32 values.
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(__uint_as_float(x) - __uint_as_float(hi)));
+}
+// d += a b to fp32's accuracy: the two small cross products, then the large one.
+__device__ __forceinline__ void mma_f32(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    uint32_t ah[4], al[4], bh0, bh1, bl0, bl1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
+    split_tf32(b0, bh0, bl0);
+    split_tf32(b1, bh1, bl1);
+    mma_tf32(d, al, bh0, bh1);
+    mma_tf32(d, ah, bl0, bl1);
+    mma_tf32(d, ah, bh0, bh1);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+// Sizes of one instantiation. NT: tiles of 8 query heads that a block works on at once.
+//  - the ring holds 96 KB of rows an SM or more in flight, beside what is being read;
+//  - two blocks of 4 warps an SM while the ring and the queries fit twice (one block's join
+//    overlaps the other's stream), else one;
+//  - a stage has room for a segment's queries, as every tile in flight may begin a segment.
+template <typename T, int D, int NT>
+struct Shape {
+    static constexpr int kRowBytes = D * (int)sizeof(T);
+    static constexpr int kPieces = kRowBytes / 16;               // 16-byte pieces of a row
+    static constexpr bool kWide = sizeof(T) == 2 ? D == 128 && NT > 1 : D == 64 && NT > 1;
+    static constexpr int W = kWide ? 8 : 4;
+    static constexpr int S = sizeof(T) == 2 && D == 64 ? 5 : 3;
+    static constexpr int kPerSm = kWide || (sizeof(T) == 4 && D == 128) ? 1 : 2;
+    static constexpr int kTile = 16 * W;                         // slots of a tile
+    static constexpr int kStage = 32 * kRowBytes;                // a warp's K and V rows
+    static constexpr int kQ = 8 * NT * kRowBytes;                // a segment's queries
+    static constexpr int kRegs = D / 4 * NT;                     // output registers a lane (D/16 x 4 x NT)
+    static constexpr int kPart = kRegs * 32 + 16 * NT;           // floats of a part: O, m, l
+    static constexpr size_t kSmem = (size_t)S * (W * kStage + kQ) + kMergeFloats * 4 +
+                                    (2 * W * 8 * NT + W * S) * 4;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kPerSm == 1 || 2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
+};
+
+struct Params {
+    PagedCache c;
+    const void *q, *z;
+    const int32_t* seqlens;
+    float scale_log2;
+    void* o;
+    int N, Hq, H, G, GT;             // GT: head tiles of a group
+    int max_len;
+    int most_blocks;
+    int* meta;                       // [blocks][4]: n, head * GT + gt, last block of a segment to join
+    float* parts;                    // [2 blocks][kPart]: a block's first and last segments' parts
+    // for acc: scores (log2 units) [tile][GS][kTile], {max, 1 / sum} [N, Hq], and tiles of the
+    // sequences before n [N + 1]
+    float* scores;
+    float2* stats;
+    int* tiles_before;
+    int GS;                          // heads of a tile's scores: min(G, 8 NT)
+    float* acc;
+    int slots;
+};
+
+// Which head, output channel a lane's register r of a part stands for (r = ((nt, mt), c)).
+template <int D>
+__device__ __forceinline__ void part_coord(int r, int lane, int& head, int& ch) {
+    const int c = r & 3, mt = (r >> 2) % (D / 16), nt = (r >> 2) / (D / 16);
+    head = nt * 8 + 2 * (lane & 3) + (c & 1);
+    ch = mt * 16 + (lane >> 2) + 8 * (c >> 1);
 }
 
-// One CTA per (sequence, query head); w holds [N * Hq, max_len] scores, then weights.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
-    __shared__ float s_q[128], s_buf[kThreads / 32];
-    const int64_t nh = blockIdx.x, n = nh / a.Hq;
-    const int hkv = (int)(nh % a.Hq) / (a.Hq / a.H), d = a.d;
-    const int len = checked_len(a.seqlens[n], a.max_len, a.c.err);
-    float* w = static_cast<float*>(a.workspace) + nh * a.max_len;
-    if (threadIdx.x < d) s_q[threadIdx.x] = to_f32(static_cast<const T*>(a.q)[nh * d + threadIdx.x]) * a.scale;
-    __syncthreads();
-    float m = -INFINITY;
-    for (int j = threadIdx.x; j < len; j += kThreads) {
-        const int64_t off = slot_offset(a.c, n, j);
-        float s = -INFINITY;
-        if (off >= 0) {
-            const T* k = static_cast<const T*>(a.c.k) + off + hkv * a.c.head_stride;
-            s = 0.f;
-            for (int c = 0; c < d; ++c) s = fmaf(s_q[c], to_f32(k[c]), s);
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(Shape<T, D, NT>::W * 32, Shape<T, D, NT>::kPerSm)
+paged_decode_kernel(const Params p) {
+    using X = Shape<T, D, NT>;
+    constexpr int W = X::W, S = X::S, kThreads = W * 32, kTile = X::kTile;
+    constexpr bool kBf16 = sizeof(T) == 2;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* s_ring = smem;                                        // [W][S][K 16 rows, V 16 rows]
+    uint8_t* s_q = s_ring + (size_t)S * W * X::kStage;             // [S][8 NT rows]
+    float* s_merge = reinterpret_cast<float*>(s_q + (size_t)S * X::kQ);
+    float* s_m = s_merge + kMergeFloats;                           // [W][8 NT]
+    float* s_l = s_m + W * 8 * NT;
+    uint32_t* s_live = reinterpret_cast<uint32_t*>(s_l + W * 8 * NT);   // [W][S] slots to attend to
+    __shared__ int64_t s_scan[W];
+    __shared__ int64_t s_first[2];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int heads = p.H * p.GT;                                  // segments of a sequence
+    const T* q = static_cast<const T*>(p.q);
+
+    // ---- the block's range of tiles
+    auto len_of = [&](int n) { return checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err); };
+    auto tiles_of = [&](int len) { return (len + kTile - 1) / kTile; };
+    auto block_scan = [&](int64_t x, int64_t* total) {             // exclusive
+        int64_t y = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += u;
         }
-        w[j] = s;
-        m = fmaxf(m, s);
+        __syncthreads();
+        if (lane == 31) s_scan[warp] = y;
+        __syncthreads();
+        int64_t before = 0, sum = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) before += s_scan[w];
+            sum += s_scan[w];
+        }
+        *total = sum;
+        return before + y - x;
+    };
+    int64_t total = 0, mine = 0, excl;
+    for (int n = tid; n < p.N; n += kThreads) mine += tiles_of(len_of(n));
+    excl = block_scan(mine, &total);
+    const int64_t work = total * heads;
+    const int C = split_blocks(work, p.most_blocks), b = blockIdx.x;
+    // sequences of length 0 have no tiles: their outputs are written here
+    for (int n = b; n < p.N; n += gridDim.x)
+        if (len_of(n) == 0)
+            for (int e = tid; e < p.Hq * D; e += kThreads)
+                static_cast<T*>(p.o)[(int64_t)n * p.Hq * D + e] = from_f32<T>(0.f);
+    if (tid == 0 && b < kMaxBlocks) p.meta[4 * b + 2] = -1;
+    if (b >= C) return;
+    const int64_t t0 = split_begin(work, C, b);
+    const int count = (int)(split_begin(work, C, b + 1) - t0);
+    {
+        const int64_t target = t0 / heads;                         // tiles of earlier sequences <= target
+        int64_t run = 0;
+        for (int base = 0; base < p.N; base += kThreads) {
+            const int n = base + tid;
+            int64_t x, sum, before;
+            if (p.N <= kThreads) {                                 // the scan above was this one
+                x = mine; sum = total; before = excl;
+            } else {
+                x = n < p.N ? tiles_of(len_of(n)) : 0;
+                before = block_scan(x, &sum);
+            }
+            if (n < p.N && b == 0 && p.tiles_before != nullptr) p.tiles_before[n] = (int)(run + before);
+            if (x > 0 && run + before <= target && target < run + before + x) {
+                s_first[0] = n;
+                s_first[1] = run + before;
+            }
+            run += sum;
+            if (run > target && !(b == 0 && p.tiles_before != nullptr)) break;
+        }
+        __syncthreads();
     }
-    m = block_reduce(m, true, s_buf);
-    if (m == -INFINITY) m = 0.f;
-    float l = 0.f;
-    for (int j = threadIdx.x; j < len; j += kThreads) l += (w[j] = expf(w[j] - m));
-    l = block_reduce(l, false, s_buf);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int j = threadIdx.x; j < len; j += kThreads) w[j] *= inv;
-    __syncthreads();
-    if (threadIdx.x >= d) return;
-    float o = 0.f;
-    for (int j = 0; j < len; ++j) {
-        const int64_t off = slot_offset(a.c, n, j);
-        if (off < 0) continue;
-        o = fmaf(w[j], to_f32(static_cast<const T*>(a.c.v)[off + hkv * a.c.head_stride + threadIdx.x]), o);
+
+    // ---- a position in the order of tiles: sequence, head (with its head tile), tile
+    struct Cursor { int n, head, tile, len, tiles; };
+    auto next = [&](Cursor& u) {
+        if (++u.tile < u.tiles) return;
+        u.tile = 0;
+        if (++u.head < heads) return;
+        u.head = 0;
+        do {
+            ++u.n;
+            u.len = u.n < p.N ? len_of(u.n) : 1;
+        } while (u.len == 0);
+        u.tiles = tiles_of(u.len);
+    };
+    Cursor cur;
+    cur.n = (int)s_first[0];
+    cur.len = len_of(cur.n);
+    cur.tiles = tiles_of(cur.len);
+    {
+        const int64_t in_seq = t0 - s_first[1] * heads;
+        cur.head = (int)(in_seq / cur.tiles);
+        cur.tile = (int)(in_seq % cur.tiles);
     }
-    if (a.z != nullptr) o /= 1.f + expf(-to_f32(static_cast<const T*>(a.z)[nh * d + threadIdx.x]));
-    static_cast<T*>(a.o)[nh * d + threadIdx.x] = from_f32<T>(o);
+
+    // ---- loads. `ahead` is the tile whose page numbers are being fetched: lane l < 16 holds slot
+    // l of the warp's 16, and its page number is used only when the tile is loaded.
+    Cursor ahead = cur;
+    int page = -1, row = 0, fetched = 0, loaded = 0, seg_loaded = -1;
+    bool live = false;
+    auto fetch = [&]() {
+        live = false;
+        if (fetched < count && lane < 16) {
+            const int slot = ahead.tile * kTile + warp * 16 + lane;
+            if (slot < ahead.len) {
+                live = true;
+                row = slot % p.c.page_size;
+                page = __ldg(p.c.block_table + (int64_t)ahead.n * p.c.max_pages + slot / p.c.page_size);
+            }
+        }
+    };
+    uint8_t* ring = s_ring + (size_t)warp * S * X::kStage;
+    auto load = [&]() {          // tile `loaded` (= fetched): its rows, and its queries if it begins a segment
+        if (loaded < count) {
+            const int st = loaded % S, hkv = ahead.head / p.GT, gt = ahead.head % p.GT;
+            if (live && (page < 0 || page >= p.c.num_pages)) {
+                atomicOr(p.c.err, kErrIndex);
+                live = false;
+            }
+            const uint32_t mask = __ballot_sync(0xffffffffu, live);
+            if (lane == 0) s_live[warp * S + st] = mask;
+            const int64_t off = live ? (page * p.c.page_stride + row * p.c.slot_stride +
+                                        hkv * p.c.head_stride) * (int64_t)sizeof(T) : 0;
+            const uint32_t dst = smem_u32(ring + st * X::kStage);
+            constexpr int kRows = 32 / X::kPieces;       // rows a warp instruction covers
+            const int piece = lane % X::kPieces;
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += kRows) {
+                const int r = r0 + lane / X::kPieces;
+                const int64_t from = __shfl_sync(0xffffffffu, off, r) + piece * 16;
+                const bool ok = mask >> r & 1;
+                const uint32_t to = dst + r * X::kRowBytes + ((piece ^ (r & 7)) << 4);
+                cp_async16(to, static_cast<const uint8_t*>(p.c.k) + (ok ? from : 0), ok);
+                cp_async16(to + 16 * X::kRowBytes, static_cast<const uint8_t*>(p.c.v) + (ok ? from : 0), ok);
+            }
+            if (loaded == 0 || ahead.tile == 0) {
+                ++seg_loaded;
+                const uint32_t qd = smem_u32(s_q + (size_t)(seg_loaded % S) * X::kQ);
+                for (int e = tid; e < 8 * NT * X::kPieces; e += kThreads) {
+                    const int g = e / X::kPieces, pc = e % X::kPieces, hg = gt * 8 * NT + g;
+                    const bool ok = hg < p.G;
+                    const T* src = q + ((int64_t)ahead.n * p.Hq + hkv * p.G + (ok ? hg : 0)) * D;
+                    cp_async16(qd + g * X::kRowBytes + ((pc ^ (g & 7)) << 4),
+                               reinterpret_cast<const uint8_t*>(src) + pc * 16, ok);
+                }
+            }
+            ++loaded;
+            ++fetched;
+            if (fetched < count) next(ahead);
+            fetch();
+        }
+        cp_commit();
+    };
+    fetch();
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) load();
+
+    // ---- the tiles
+    float out[NT][D / 16][4], m[NT][2], l[NT][2];
+    auto reset = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) out[nt][mt][c] = 0.f;
+        }
+    };
+    reset();
+    int seg = 0;
+    bool from_start = cur.tile == 0;               // the segment begins in this block
+    for (int i = 0; i < count; ++i) {
+        cp_wait<S - 2>();
+        __syncwarp();
+        load();                                    // into the stage read in the step before
+        const int st = i % S;
+        if (i == 0 || cur.tile == 0) __syncthreads();              // the segment's queries are there
+        const uint32_t kd = smem_u32(ring + st * X::kStage), vd = kd + 16 * X::kRowBytes;
+        const uint32_t qd = smem_u32(s_q + (size_t)(seg % S) * X::kQ);
+        const uint32_t mask = s_live[warp * S + st];
+
+        // S^T = K Q^T: rows slots, columns heads. Two accumulators halve the chain.
+        float s[NT][4], s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
+        const int ar = lane & 15, ax = ar & 7, bx = lane & 7;
+#pragma unroll
+        for (int ks = 0; ks < X::kPieces / 2; ks += 2) {
+            uint32_t a0[4], a1[4];
+            ldsm4(kd + ar * X::kRowBytes + (((2 * ks + (lane >> 4)) ^ ax) << 4), a0);
+            ldsm4(kd + ar * X::kRowBytes + (((2 * ks + 2 + (lane >> 4)) ^ ax) << 4), a1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t bq[4];
+                ldsm4(qd + (nt * 8 + bx) * X::kRowBytes + (((2 * ks + (lane >> 3)) ^ bx) << 4), bq);
+                if constexpr (kBf16) {
+                    mma_bf16(s[nt], a0, bq[0], bq[1]);
+                    mma_bf16(s2[nt], a1, bq[2], bq[3]);
+                } else {
+                    mma_f32(s[nt], a0, bq[0], bq[1]);
+                    mma_f32(s2[nt], a1, bq[2], bq[3]);
+                }
+            }
+        }
+        const bool ok0 = mask >> (lane >> 2) & 1, ok1 = mask >> ((lane >> 2) + 8) & 1;
+        float corr[NT][2];
+        bool moved = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float x[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                x[c] = (c < 2 ? ok0 : ok1) ? (s[nt][c] + s2[nt][c]) * p.scale_log2 : -INFINITY;
+            if (p.scores != nullptr) {
+                float* w = p.scores + (t0 + i) * p.GS * kTile + warp * 16 + (lane >> 2);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int g = nt * 8 + 2 * (lane & 3) + (c & 1);
+                    if (g < p.GS) w[g * kTile + 8 * (c >> 1)] = x[c];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(x[e], x[e + 2]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float mn = fmaxf(m[nt][e], mx), base = mn == -INFINITY ? 0.f : mn;
+                corr[nt][e] = exp2_fast(m[nt][e] - base);
+                moved |= mn != m[nt][e];
+                m[nt][e] = mn;
+                s[nt][e] = exp2_fast(x[e] - base);
+                s[nt][e + 2] = exp2_fast(x[e + 2] - base);
+                l[nt][e] = l[nt][e] * corr[nt][e] + s[nt][e] + s[nt][e + 2];
+            }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) out[nt][mt][c] *= corr[nt][c & 1];
+        }
+        // O^T += V^T P^T: rows channels, columns heads
+        if constexpr (kBf16) {
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const __nv_bfloat162 w = __floats2bfloat162_rn(s[nt][2 * e], s[nt][2 * e + 1]);
+                    pb[nt][e] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+                }
+            const int vr = (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                uint32_t a[4];
+                ldsm4_t(vd + vr * X::kRowBytes + (((2 * mt + ((lane >> 3) & 1)) ^ (vr & 7)) << 4), a);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_bf16(out[nt][mt], a, pb[nt][0], pb[nt][1]);
+            }
+        } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {                 // 8 slots each
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {                  // slot lane % 4 + 4 e, head lane / 4
+                        const int from = ((lane & 3) + 4 * e) * 4 + (lane >> 3);
+                        const float u = __shfl_sync(0xffffffffu, s[nt][2 * half], from);
+                        const float v = __shfl_sync(0xffffffffu, s[nt][2 * half + 1], from);
+                        pb[nt][e] = __float_as_uint((lane >> 2) & 1 ? v : u);
+                    }
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {                  // channel + 8 (c & 1), slot + 4 (c >> 1)
+                        const int r = 8 * half + (lane & 3) + 4 * (c >> 1);
+                        const int ch = mt * 16 + (lane >> 2) + 8 * (c & 1);
+                        a[c] = *reinterpret_cast<const uint32_t*>(
+                            ring + st * X::kStage + (16 + r) * X::kRowBytes +
+                            (((ch >> 2) ^ (r & 7)) << 4) + (ch & 3) * 4);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f32(out[nt][mt], a, pb[nt][0], pb[nt][1]);
+                }
+            }
+        }
+
+        // ---- the segment's end, or the block's
+        const bool to_end = cur.tile + 1 == cur.tiles;
+        if (to_end || i + 1 == count) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+                    if (lane < 4) {
+                        s_m[warp * 8 * NT + nt * 8 + 2 * lane + e] = m[nt][e];
+                        s_l[warp * 8 * NT + nt * 8 + 2 * lane + e] = l[nt][e];
+                    }
+                }
+            __syncthreads();
+            const bool whole = from_start && to_end;
+            // a part that began earlier, or spans the block, is its first; one that goes on its last
+            float* part = p.parts + (int64_t)(2 * b + (from_start ? 1 : 0)) * X::kPart;
+            float sum[NT][2], mul[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = nt * 8 + 2 * (lane & 3) + e;
+                    float mx = -INFINITY, sm = 0.f;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w * 8 * NT + h]);
+                    const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        sm += s_l[w * 8 * NT + h] * exp2_fast(s_m[w * 8 * NT + h] - base);
+                    mul[nt][e] = exp2_fast(m[nt][e] - base);
+                    sum[nt][e] = sm;
+                    if (warp == 0 && lane < 4) {
+                        if (!whole) {
+                            part[X::kRegs * 32 + h] = mx;
+                            part[X::kRegs * 32 + 8 * NT + h] = sm;
+                        } else if (p.stats != nullptr && (cur.head % p.GT) * 8 * NT + h < p.G) {
+                            const int64_t at = (int64_t)cur.n * p.Hq + cur.head / p.GT * p.G +
+                                               (cur.head % p.GT) * 8 * NT + h;
+                            p.stats[at] = make_float2(base, sm > 0.f ? 1.f / sm : 0.f);
+                        }
+                    }
+                }
+            // sum the warps' outputs, kRound registers at a time; each warp finishes its share
+            constexpr int kRound = kMergeFloats / kThreads, kShare = kRound / W;
+            static_assert(X::kRegs % kRound == 0 && kRound % W == 0, "rounds");
+            const float* flat = &out[0][0][0];
+#pragma unroll
+            for (int r0 = 0; r0 < X::kRegs; r0 += kRound) {
+                if (r0 > 0) __syncthreads();
+#pragma unroll
+                for (int r = 0; r < kRound; ++r) {
+                    const int nt = (r0 + r) / (D / 4);
+                    s_merge[(warp * kRound + r) * 32 + lane] = flat[r0 + r] * mul[nt][r & 1];
+                }
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < kShare; ++u) {
+                    const int r = warp * kShare + u;
+                    float y = 0.f;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) y += s_merge[(w * kRound + r) * 32 + lane];
+                    if (!whole) {
+                        part[(r0 + r) * 32 + lane] = y;
+                        continue;
+                    }
+                    int h, ch;
+                    part_coord<D>(r0 + r, lane, h, ch);
+                    const int hg = (cur.head % p.GT) * 8 * NT + h;
+                    if (hg >= p.G) continue;
+                    const int64_t at = ((int64_t)cur.n * p.Hq + cur.head / p.GT * p.G + hg) * D + ch;
+                    float sm = 0.f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (nt == h >> 3) sm = sum[nt][h & 1];
+                    y = sm > 0.f ? y / sm : 0.f;
+                    if (p.z != nullptr) y *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
+                    static_cast<T*>(p.o)[at] = from_f32<T>(y);
+                }
+            }
+            if (!whole && from_start && tid == 0) {            // this block's last: join it with the next ones'
+                const int64_t last = t0 + i + (cur.tiles - 1 - cur.tile);
+                p.meta[4 * b] = cur.n;
+                p.meta[4 * b + 1] = cur.head;
+                p.meta[4 * b + 2] = split_block_of(work, C, last);
+            }
+            reset();
+            ++seg;
+            from_start = true;
+        }
+        if (i + 1 < count) next(cur);
+    }
+    cp_wait<0>();
 }
 
-// acc[n, h, j] += the sum of the group's weights.
-__global__ void __launch_bounds__(kThreads) weights_kernel(const DecodeArgs a) {
-    const int64_t nh = blockIdx.x, n = nh / a.H;
-    const int h = (int)(nh % a.H), g = a.Hq / a.H;
-    const int len = checked_len(a.seqlens[n], a.max_len, a.c.err);
-    const float* w = static_cast<const float*>(a.workspace) + (n * a.Hq + h * g) * (int64_t)a.max_len;
-    for (int j = threadIdx.x; j < len; j += kThreads) {
-        float s = 0.f;
-        for (int i = 0; i < g; ++i) s += w[(int64_t)i * a.max_len + j];
-        a.acc[nh * a.slots + j] += s;
+// Joins the parts of the segment that begins in block blockIdx.x and goes on in later ones.
+// blockIdx.y: eight of the part's registers (two blocks of 16 channels of one tile of 8 heads).
+constexpr int kJoinWarps = 4;
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Params p) {
+    using X = Shape<T, D, NT>;
+    __shared__ float s_f[kMaxBlocks][8];
+    __shared__ float s_sum[8], s_top[8];
+    __shared__ float s_o[kJoinWarps][8][32];
+    const int b = blockIdx.x, r0 = blockIdx.y * 8, nt = r0 / (D / 4);
+    const int last = p.meta[4 * b + 2];
+    if (last < 0) return;
+    const int n = p.meta[4 * b], head = p.meta[4 * b + 1], k = last - b + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto part = [&](int j) { return p.parts + (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * X::kPart; };
+    for (int e = tid; e < k * 8; e += kJoinWarps * 32)
+        s_f[e >> 3][e & 7] = part(e >> 3)[X::kRegs * 32 + nt * 8 + (e & 7)];
+    __syncthreads();
+    {                                          // 16 threads a head: the maximum, then factors and sum
+        const int h = tid >> 4, u = tid & 15;
+        float mx = -INFINITY, sm = 0.f;
+        for (int j = u; j < k; j += 16) mx = fmaxf(mx, s_f[j][h]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float base = mx == -INFINITY ? 0.f : mx;
+        for (int j = u; j < k; j += 16) {
+            const float f = exp2_fast(s_f[j][h] - base);
+            s_f[j][h] = f;
+            sm += f * part(j)[X::kRegs * 32 + 8 * NT + nt * 8 + h];
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sm += __shfl_xor_sync(0xffffffffu, sm, o);
+        if (u == 0) {
+            s_sum[h] = sm;
+            s_top[h] = base;
+        }
     }
+    __syncthreads();
+    float y[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) y[r] = 0.f;
+    for (int j = warp; j < k; j += kJoinWarps) {
+        const float* src = part(j) + r0 * 32 + lane;
+        const float f0 = s_f[j][2 * (lane & 3)], f1 = s_f[j][2 * (lane & 3) + 1];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) y[r] += src[r * 32] * (r & 1 ? f1 : f0);
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s_o[warp][r][lane] = y[r];
+    __syncthreads();
+    const int g0 = head / p.GT * p.G, first = (head % p.GT) * 8 * NT;
+#pragma unroll
+    for (int u = 0; u < 8 / kJoinWarps; ++u) {
+        const int r = warp * (8 / kJoinWarps) + u;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) v += s_o[w][r][lane];
+        int h, ch;
+        part_coord<D>(r0 + r, lane, h, ch);
+        if (first + h >= p.G) continue;
+        const float sm = s_sum[h & 7];
+        v = sm > 0.f ? v / sm : 0.f;
+        const int64_t at = ((int64_t)n * p.Hq + g0 + first + h) * D + ch;
+        if (p.z != nullptr) v *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
+        static_cast<T*>(p.o)[at] = from_f32<T>(v);
+    }
+    if (p.stats != nullptr && r0 % (D / 4) == 0 && tid < 8 && first + nt * 8 + tid < p.G)
+        p.stats[(int64_t)n * p.Hq + g0 + first + nt * 8 + tid] =
+            make_float2(s_top[tid], s_sum[tid] > 0.f ? 1.f / s_sum[tid] : 0.f);
+}
+
+// acc[n, h, j] += sum over the group's heads of exp2(score - max) / sum.
+constexpr int kWeightThreads = 128;
+template <int kTile>
+__global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(const Params p, int NT8) {
+    const int chunks = (p.max_len + kWeightThreads - 1) / kWeightThreads;
+    const int64_t all = (int64_t)p.N * p.H * chunks;
+    for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
+        const int64_t nh = w / chunks, n = nh / p.H;
+        const int j = (int)(w % chunks) * kWeightThreads + threadIdx.x, h = (int)(nh % p.H);
+        const int len = checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err);
+        if (j >= len) continue;
+        const int tiles = (len + kTile - 1) / kTile;
+        const int64_t tile = ((int64_t)p.tiles_before[n] * p.H + (int64_t)h * tiles) * p.GT + j / kTile;
+        const float2* st = p.stats + n * p.Hq + h * p.G;
+        float sum = 0.f;
+        for (int gt = 0; gt < p.GT; ++gt) {
+            const float* s = p.scores + (tile + (int64_t)gt * tiles) * p.GS * kTile + j % kTile;
+            const int gs = min(NT8, p.G - gt * NT8);
+            for (int g = 0; g < gs; ++g) {
+                const float2 t = st[gt * NT8 + g];
+                sum = fmaf(exp2_fast(s[g * kTile] - t.x), t.y, sum);
+            }
+        }
+        p.acc[nh * p.slots + j] += sum;
+    }
+}
+
+// NT for a group of G heads: one tile of 8, two, or four (fp32: two at most, for its ring).
+int head_tiles(int64_t G, bool bf16) { return G <= 8 ? 1 : (G <= 16 || !bf16) ? 2 : 4; }
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct Layout {
+    size_t meta, parts, tiles_before, stats, scores, total;
+};
+Layout layout(int64_t N, int64_t Hq, int64_t H, int64_t max_len, bool with_acc, int NT, size_t part_floats) {
+    const int64_t G = Hq / H, GT = (G + 8 * NT - 1) / (8 * NT), GS = G < 8 * NT ? G : 8 * NT;
+    Layout l;
+    l.meta = 0;
+    l.parts = up256(kMaxBlocks * 4 * sizeof(int));
+    l.tiles_before = l.parts + up256(2 * kMaxBlocks * part_floats * sizeof(float));
+    l.stats = l.tiles_before + (with_acc ? up256(N * sizeof(int)) : 0);
+    l.scores = l.stats + (with_acc ? up256(N * Hq * sizeof(float2)) : 0);
+    const int64_t padded = (max_len + 127) / 128 * 128;          // whole tiles of 64 or 128 slots
+    l.total = l.scores + (with_acc ? (size_t)(N * H * GT) * padded * GS * sizeof(float) : 0);
+    return l;
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
+    using X = Shape<T, D, NT>;
+    const int sms = sm_count();
+    if (sms == 0) return cudaErrorInvalidDevice;
+    const Layout l = layout(a.N, a.Hq, a.H, a.max_len, a.acc != nullptr, NT, X::kPart);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    Params p;
+    p.c = a.c;
+    p.q = a.q; p.z = a.z;
+    p.seqlens = a.seqlens;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.o = a.o;
+    p.N = a.N; p.Hq = a.Hq; p.H = a.H;
+    p.G = a.Hq / a.H;
+    p.GT = (p.G + 8 * NT - 1) / (8 * NT);
+    p.max_len = a.max_len;
+    p.most_blocks = sms * X::kPerSm < kMaxBlocks ? sms * X::kPerSm : kMaxBlocks;
+    p.meta = reinterpret_cast<int*>(ws + l.meta);
+    p.parts = reinterpret_cast<float*>(ws + l.parts);
+    p.tiles_before = a.acc ? reinterpret_cast<int*>(ws + l.tiles_before) : nullptr;
+    p.stats = a.acc ? reinterpret_cast<float2*>(ws + l.stats) : nullptr;
+    p.scores = a.acc ? reinterpret_cast<float*>(ws + l.scores) : nullptr;
+    p.GS = p.G < 8 * NT ? p.G : 8 * NT;
+    p.acc = a.acc;
+    p.slots = a.slots;
+    cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<T, D, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X::kSmem);
+    if (e != cudaSuccess) return e;
+    paged_decode_kernel<T, D, NT><<<p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
+    paged_join_kernel<T, D, NT><<<dim3(p.most_blocks, X::kRegs / 8), kJoinWarps * 32, 0, stream>>>(p);
+    if (a.acc != nullptr && a.max_len > 0) {
+        const int64_t all = (int64_t)a.N * a.H * ((a.max_len + kWeightThreads - 1) / kWeightThreads);
+        const unsigned grid = (unsigned)(all < sms * 16 ? all : sms * 16);
+        paged_weights_kernel<X::kTile><<<grid, kWeightThreads, 0, stream>>>(p, 8 * NT);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
+    switch (head_tiles(a.Hq / a.H, sizeof(T) == 2)) {
+        case 1: return launch_t<T, D, 1>(a, stream);
+        case 2: return launch_t<T, D, 2>(a, stream);
+    }
+    if constexpr (sizeof(T) == 2) return launch_t<T, D, 4>(a, stream);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-bool paged_decode_workspace(int64_t N, int64_t Hq, int64_t, int, int64_t max_len, bool, size_t* bytes) {
-    const double want = (double)N * Hq * max_len * 4;
-    if (want > 9e18) return false;
-    *bytes = (size_t)(N * Hq) * (size_t)max_len * 4;
+bool paged_decode_workspace(int64_t N, int64_t Hq, int64_t H, int d, int64_t max_len, bool with_acc,
+                            size_t* bytes) {
+    const double scores = (double)N * H * (Hq / H + 32) * (max_len + 128) * 4;
+    if (N * Hq > INT32_MAX || scores > 4e18) return false;
+    size_t most = 0;                     // whichever io: bf16 and fp32 differ in their head tiles
+    for (bool bf16 : {false, true}) {
+        const int NT = head_tiles(Hq / H, bf16);
+        const size_t t = layout(N, Hq, H, max_len, with_acc, NT, (size_t)(d / 4 * 32 + 16) * NT).total;
+        if (t > most) most = t;
+    }
+    *bytes = most;
     return true;
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t stream) {
     if (a.N == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)(a.N * a.Hq);
-    if (a.io == Io::BF16) decode_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-    else decode_kernel<float><<<grid, kThreads, 0, stream>>>(a);
-    if (a.acc != nullptr) weights_kernel<<<(unsigned)(a.N * a.H), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (a.io == Io::BF16)
+        return a.d == 128 ? launch_d<__nv_bfloat16, 128>(a, stream) : launch_d<__nv_bfloat16, 64>(a, stream);
+    return a.d == 128 ? launch_d<float, 128>(a, stream) : launch_d<float, 64>(a, stream);
 }
 
 }  // namespace kda

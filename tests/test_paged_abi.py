@@ -3,13 +3,16 @@ workspace queries."""
 from __future__ import annotations
 
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 from kimi_delta_attention_32_b200 import build as kbuild
 from kimi_delta_attention_32_b200 import kda
-from test_abi import FAKE, MIS, _cu_host
+from test_abi import FAKE, MIS, ROOT, _cu_host
 
 INV, UNS, WS = kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED, kda.KDA_ERR_WORKSPACE
 ODD = ctypes.c_void_p(0x10002)           # not even 4-byte aligned
@@ -135,6 +138,39 @@ def test_workspace_queries(lib):
     assert size(4, 0, 1000, 10, ctypes.byref(out)) == INV
     assert size(4, 8, 1000, 400, None) == INV
     assert size(4, 8, 1000, 400, ctypes.byref(out)) == 0
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_split_covers_every_tile_once(tmp_path):
+    """The division of tiles over blocks: contiguous, complete, none empty, sizes one apart at
+    most, and split_block_of is its inverse."""
+    src = tmp_path / "split.cpp"
+    src.write_text(r"""
+#include "decode_split.h"
+using namespace kda;
+int main() {
+    const int64_t works[] = {1, 2, 3, 7, 147, 148, 149, 295, 296, 297, 320, 1000, 12345, 65536,
+                             131072, 1 << 20, (1ll << 40) + 12345};
+    const int mosts[] = {1, 2, 37, 148, 160, 296, 320};
+    for (int64_t W : works)
+        for (int most : mosts) {
+            const int C = split_blocks(W, most);
+            if (C < 1 || C > most || C > W) return 1;
+            if (split_begin(W, C, 0) != 0 || split_begin(W, C, C) != W) return 2;
+            for (int c = 0; c < C; ++c) {
+                const int64_t a = split_begin(W, C, c), b = split_begin(W, C, c + 1);
+                if (b - a < W / C || b - a > W / C + 1 || b <= a) return 3;
+                if (split_block_of(W, C, a) != c || split_block_of(W, C, b - 1) != c ||
+                    split_block_of(W, C, a + (b - a) / 2) != c) return 4;
+            }
+        }
+    return 0;
+}
+""")
+    exe = tmp_path / "split"
+    inc = os.path.join(ROOT, "kimi_delta_attention_32_b200", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-I", inc, str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)], timeout=60).returncode == 0
 
 
 def test_index_status_has_a_text(lib):
