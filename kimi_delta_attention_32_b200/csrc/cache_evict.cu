@@ -4,14 +4,32 @@
 // Attention：每 4 层只留 1 层全注意力". The pages have no eviction.)
 //
 // Entries rank by a 32-bit key: guarded ones first, then larger acc; equal keys by slot. The keep
-// best stay. Those behind slot keep move into the free slots before it, both in slot order: the
-// number of rows that move is the number that are evicted below keep, however long the cache.
+// best stay. Those behind slot keep move into the free slots before it ("holes"), both in slot
+// order, so the rows that move are only as many as were evicted below keep, however long the
+// cache; keeping the slots in order instead would move nearly every row behind the first hole.
+//
+// Select: one thread-block cluster per (sequence, head), of 1 to 8 blocks by the cache's length.
+// Each block reads its part of acc and pos once, into 32-bit keys in shared memory (up to 49152 a
+// block; longer caches are read again in every pass), and all passes run on those: three of a
+// radix select (11, 11 and 10 bits from the top; the blocks' histograms are summed through
+// distributed shared memory), one that counts ties, one that counts what is kept, and one that
+// writes the lists of holes and of the entries that fill them. Integers only: no order of
+// atomics can show. It is bound by the latency of its dozen barriers and, for long caches, by
+// shared-memory atomics; the traffic is one read of acc and pos.
+// Move: the whole GPU copies the listed rows, 64 entries a block, bound by HBM (each moved row is
+// read and written once).
+#include <cooperative_groups.h>
+
 #include "paged.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
+namespace cg = cooperative_groups;
+
+constexpr int kMaxKeys = 49152;           // keys of one block in shared memory: 192 KB
+constexpr int kBins = 2048;               // histogram of one pass (three of them: 24 KB)
+constexpr int kMaxCluster = 8;
 
 // Rank key of an entry: order-preserving bits of the fp32 weight (NaN lowest, -0 equal to 0).
 __device__ __forceinline__ uint32_t rank_key(float acc, int64_t pos, int n_first, int64_t recent_from) {
@@ -21,10 +39,20 @@ __device__ __forceinline__ uint32_t rank_key(float acc, int64_t pos, int n_first
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Exclusive prefix sum of x over the CTA; *total receives the sum.
+struct SelectArgs {
+    EvictArgs e;
+    int* counts;              // [N * H] moves
+    int* lists;               // [N * H][2][most]: holes, then the entries that fill them
+    int most;
+    int keys;                 // keys a block holds in shared memory, 0: none
+};
+
+// Exclusive prefix sum of x over the block; *total receives the sum.
+template <int kThreads>
 __device__ __forceinline__ int block_scan(int x, int* buf, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int y = x;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int z = __shfl_up_sync(0xffffffffu, y, o);
         if (lane >= o) y += z;
@@ -33,6 +61,7 @@ __device__ __forceinline__ int block_scan(int x, int* buf, int* total) {
     if (lane == 31) buf[warp] = y;
     __syncthreads();
     int before = 0, sum = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += buf[w];
         sum += buf[w];
@@ -41,83 +70,208 @@ __device__ __forceinline__ int block_scan(int x, int* buf, int* total) {
     return before + y - x;
 }
 
-// One CTA per (sequence, head): the keep-th key by bisection over its bits, then the lists of
-// holes and of the entries that fill them. lists: [N * H][2][most] and counts [N * H].
-__global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int* counts, int* lists, int most) {
-    __shared__ int s_buf[kThreads / 32];
-    const int64_t nh = blockIdx.x, n = nh / a.H;
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs s) {
+    extern __shared__ uint32_t s_keys[];
+    __shared__ int s_hist[3][kBins];
+    __shared__ int s_buf[kThreads / 32], s_pick[2];
+    __shared__ int s_share[2][2];                        // this block's counts, read by the cluster
+    const EvictArgs& a = s.e;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int64_t nh = blockIdx.x / CS, n = nh / a.H;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int len = checked_len(a.seqlens[n], a.max_len, a.c.err);
     const int64_t recent_from = (int64_t)a.positions[n] - a.n_recent, at = nh * a.slots;
-    auto key = [&](int j) { return rank_key(a.acc[at + j], a.pos[at + j], a.n_first, recent_from); };
-    if (len <= a.keep) {
-        for (int j = threadIdx.x; j < len; j += kThreads) {
-            a.acc_out[at + j] = a.acc[at + j];
-            a.pos_out[at + j] = a.pos[at + j];
+    const bool copy_acc = a.acc_out != a.acc, copy_pos = a.pos_out != a.pos;
+
+    if (len <= a.keep || a.keep == 0) {                  // nothing moves (the whole cluster agrees)
+        const int m = len <= a.keep ? len : 0;
+        for (int j = rank * kThreads + tid; j < m; j += CS * kThreads) {
+            if (copy_acc) a.acc_out[at + j] = a.acc[at + j];
+            if (copy_pos) a.pos_out[at + j] = a.pos[at + j];
         }
-        if (threadIdx.x == 0) counts[nh] = 0;
+        if (rank == 0 && tid == 0) s.counts[nh] = 0;
         return;
     }
-    // the largest T with at least keep keys >= T
-    uint32_t T = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t t = T | (1u << bit);
-        int c = 0, total;
-        for (int j = threadIdx.x; j < len; j += kThreads) c += key(j) >= t;
-        block_scan(c, s_buf, &total);
-        if (total >= a.keep) T = t;
-    }
-    int above = 0;
-    {
-        int c = 0;
-        for (int j = threadIdx.x; j < len; j += kThreads) c += key(j) > T;
-        block_scan(c, s_buf, &above);
-    }
-    const int ties = a.keep - above;          // of the entries with key T, so many lowest slots stay
-    int seen = 0, holes = 0, tails = 0;
-    int* hole = lists + nh * 2 * most;
-    int* tail = hole + most;
-    for (int j0 = 0; j0 < len; j0 += kThreads) {
-        const int j = j0 + threadIdx.x;
-        const uint32_t k = j < len ? key(j) : 0;
-        const bool tie = j < len && k == T;
-        int n_tie, n_hole, n_tail;
-        const int r = block_scan(tie, s_buf, &n_tie);
-        const bool kept = j < len && (k > T || (tie && seen + r < ties));
-        const bool is_hole = j < len && j < a.keep && !kept, is_tail = kept && j >= a.keep;
-        const int rh = block_scan(is_hole, s_buf, &n_hole), rt = block_scan(is_tail, s_buf, &n_tail);
-        if (is_hole) hole[holes + rh] = j;
-        if (is_tail) tail[tails + rt] = j;
-        seen += n_tie; holes += n_hole; tails += n_tail;
-        if (kept && j < a.keep) {
-            a.acc_out[at + j] = a.acc[at + j];
-            a.pos_out[at + j] = a.pos[at + j];
-        }
-    }
+    // the block's slots [lo, hi), a warp's a contiguous run of whole 32s of them
+    const int per_warp = ((len + CS * kThreads - 1) / (CS * kThreads)) * 32;
+    const int lo = min(len, rank * (kThreads / 32) * per_warp);
+    const int hi = min(len, lo + (kThreads / 32) * per_warp);
+    const bool held = hi - lo <= s.keys;
+    auto fresh = [&](int j) { return rank_key(a.acc[at + j], a.pos[at + j], a.n_first, recent_from); };
+    auto key = [&](int j) { return held ? s_keys[j - lo] : fresh(j); };
+
+    for (int i = tid; i < 3 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < holes; i += kThreads) {
-        a.acc_out[at + hole[i]] = a.acc[at + tail[i]];
-        a.pos_out[at + hole[i]] = a.pos[at + tail[i]];
+
+    // ---- the keep-th largest key T, 11 + 11 + 10 bits from the top; `left` of those equal to the
+    // bits found so far are still to be kept
+    uint32_t T = 0;
+    int left = a.keep;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);   // bits found already
+        for (int base = lo; base < hi; base += kThreads) {
+            const int j = base + tid;
+            uint32_t k = 0;
+            bool in = j < hi;
+            if (in) {
+                k = pass == 0 || !held ? fresh(j) : s_keys[j - lo];
+                if (pass == 0 && held) s_keys[j - lo] = k;
+                in = (k & above) == (T & above);
+            }
+            const int digit = (int)(k >> shift) & ((1 << bits) - 1);
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            if (who == 0) continue;
+            // one atomic where a warp's keys agree, as in a run of guarded or never-seen entries
+            const int lead = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
+            if (__all_sync(0xffffffffu, !in || digit == lead)) {
+                if (lane == 0) atomicAdd(&s_hist[pass][lead], __popc(who));
+            } else if (in) {
+                atomicAdd(&s_hist[pass][digit], 1);
+            }
+        }
+        cluster.sync();
+        constexpr int kPer = kBins / kThreads;           // bins a thread sums, from the top down
+        int c[kPer], mine = 0, total;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int bin = kBins - 1 - (tid * kPer + i);
+            c[i] = 0;
+            for (int r = 0; r < CS; ++r) c[i] += cluster.map_shared_rank(&s_hist[pass][0], r)[bin];
+            mine += c[i];
+        }
+        int over = block_scan<kThreads>(mine, s_buf, &total);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (over < left && left <= over + c[i]) {
+                s_pick[0] = kBins - 1 - (tid * kPer + i);
+                s_pick[1] = left - over;
+            }
+            over += c[i];
+        }
+        __syncthreads();
+        T |= (uint32_t)s_pick[0] << shift;
+        left = s_pick[1];
+        __syncthreads();
     }
-    if (threadIdx.x == 0) counts[nh] = holes;
+
+    // ---- ties: of the entries with key T the `left` lowest slots stay
+    const int w0 = min(hi, lo + warp * per_warp), w1 = min(hi, w0 + per_warp);
+    int ties = 0, total;
+    for (int j0 = w0; j0 < w1; j0 += 32)
+        ties += __popc(__ballot_sync(0xffffffffu, j0 + lane < w1 && key(j0 + lane) == T));
+    int tie_at = block_scan<kThreads>(lane == 0 ? ties : 0, s_buf, &total);
+    if (tid == 0) s_share[0][0] = total;
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) tie_at += cluster.map_shared_rank(&s_share[0][0], r)[0];
+    tie_at = __shfl_sync(0xffffffffu, tie_at, 0);
+
+    // ---- walk the warp's slots: kept or not, in slot order
+    auto walk = [&](auto&& visit) {
+        int seen = tie_at;
+        for (int j0 = w0; j0 < w1; j0 += 32) {
+            const int j = j0 + lane;
+            const uint32_t k = j < w1 ? key(j) : 0;
+            const bool tie = j < w1 && k == T;
+            const unsigned tied = __ballot_sync(0xffffffffu, tie);
+            const bool kept = j < w1 && (k > T || (tie && seen + __popc(tied & ((1u << lane) - 1)) < left));
+            seen += __popc(tied);
+            visit(j, kept);
+        }
+    };
+    int front = 0, behind = 0;                           // kept in slots < keep, and >= keep
+    walk([&](int j, bool kept) {
+        front += __popc(__ballot_sync(0xffffffffu, kept && j < a.keep));
+        behind += __popc(__ballot_sync(0xffffffffu, kept && j >= a.keep));
+    });
+    int all_front, all_behind;
+    int front_at = block_scan<kThreads>(lane == 0 ? front : 0, s_buf, &all_front);
+    int behind_at = block_scan<kThreads>(lane == 0 ? behind : 0, s_buf, &all_behind);
+    if (tid == 0) {
+        s_share[1][0] = all_front;
+        s_share[1][1] = all_behind;
+    }
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+        front_at += cluster.map_shared_rank(&s_share[1][0], r)[0];
+        behind_at += cluster.map_shared_rank(&s_share[1][0], r)[1];
+    }
+    front_at = __shfl_sync(0xffffffffu, front_at, 0);
+    behind_at = __shfl_sync(0xffffffffu, behind_at, 0);
+    int* hole = s.lists + nh * 2 * s.most;
+    int* tail = hole + s.most;
+    walk([&](int j, bool kept) {
+        const unsigned f = __ballot_sync(0xffffffffu, kept && j < a.keep);
+        const unsigned t = __ballot_sync(0xffffffffu, kept && j >= a.keep);
+        const unsigned before = (1u << lane) - 1;
+        if (j < w1 && j < a.keep && !kept) hole[j - (front_at + __popc(f & before))] = j;
+        if (kept && j >= a.keep) tail[behind_at + __popc(t & before)] = j;
+        if (kept && j < a.keep) {
+            if (copy_acc) a.acc_out[at + j] = a.acc[at + j];
+            if (copy_pos) a.pos_out[at + j] = a.pos[at + j];
+        }
+        front_at += __popc(f);
+        behind_at += __popc(t);
+    });
+    if (rank == CS - 1 && tid == kThreads - 1) s.counts[nh] = behind_at;      // the last warp's end: all
+    cluster.sync();                                      // shared memory stays until all have read it
 }
 
-__global__ void __launch_bounds__(kThreads) move_kernel(const EvictArgs a, const int* counts, const int* lists, int most, int row16) {
-    const int64_t nh = blockIdx.x, n = nh / a.H, h = nh % a.H;
-    if (h == 0 && threadIdx.x == 0)        // after every head's select has read seqlens
+constexpr int kMoveThreads = 256, kMoveRows = 64;
+template <int kPieces>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const SelectArgs s, int chunks, int esz) {
+    __shared__ int64_t s_to[kMoveRows], s_from[kMoveRows];
+    const EvictArgs& a = s.e;
+    const int64_t nh = blockIdx.x / chunks, n = nh / a.H, at = nh * a.slots;
+    const int h = (int)(nh % a.H), first = (int)(blockIdx.x % chunks) * kMoveRows, tid = threadIdx.x;
+    if (h == 0 && first == 0 && tid == 0)      // after every head's select has read seqlens
         a.seqlens_out[n] = min(checked_len(a.seqlens[n], a.max_len, a.c.err), a.keep);
-    const int* hole = lists + nh * 2 * most;
-    const int* tail = hole + most;
-    const int64_t esz = a.io == Io::BF16 ? 2 : 4;
-    const int count = counts[nh];
-    for (int i = threadIdx.x / row16; i < count; i += kThreads / row16) {
-        const int64_t to = slot_offset(a.c, n, hole[i]), from = slot_offset(a.c, n, tail[i]);
-        if (to < 0 || from < 0) continue;
-        const int64_t dst = (to + h * a.c.head_stride) * esz + (threadIdx.x % row16) * 16;
-        const int64_t src = (from + h * a.c.head_stride) * esz + (threadIdx.x % row16) * 16;
-        *reinterpret_cast<uint4*>(static_cast<char*>(a.c.k) + dst) =
-            *reinterpret_cast<const uint4*>(static_cast<const char*>(a.c.k) + src);
-        *reinterpret_cast<uint4*>(static_cast<char*>(a.c.v) + dst) =
-            *reinterpret_cast<const uint4*>(static_cast<const char*>(a.c.v) + src);
+    const int rows = min(kMoveRows, s.counts[nh] - first);
+    if (rows <= 0) return;
+    if (tid < 2 * kMoveRows) {
+        const int i = tid % kMoveRows;
+        int64_t off = -1;
+        if (i < rows) {
+            const int* list = s.lists + nh * 2 * s.most + first + i;
+            const int slot = list[tid < kMoveRows ? 0 : s.most];
+            off = slot_offset(a.c, n, slot);
+            if (off >= 0) off = (off + h * a.c.head_stride) * esz;
+            if (tid < kMoveRows) {
+                const int from = list[s.most];
+                a.acc_out[at + slot] = a.acc[at + from];
+                a.pos_out[at + slot] = a.pos[at + from];
+            }
+        }
+        (tid < kMoveRows ? s_to : s_from)[i] = off;
+    }
+    __syncthreads();
+    // K and V rows, 16 bytes a thread; a batch of loads, then its stores
+    constexpr int kStep = kMoveThreads / kPieces;        // rows a pass covers
+    constexpr int kBatch = kMoveRows / kStep < 4 ? kMoveRows / kStep : 4;
+    const int piece = (tid % kPieces) * 16;
+    char* kc = static_cast<char*>(a.c.k) + piece;
+    char* vc = static_cast<char*>(a.c.v) + piece;
+    for (int r0 = tid / kPieces; r0 < rows; r0 += kStep * kBatch) {
+        uint4 x[kBatch], y[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kStep;
+            if (r < rows && s_from[r] >= 0 && s_to[r] >= 0) {
+                x[i] = *reinterpret_cast<const uint4*>(kc + s_from[r]);
+                y[i] = *reinterpret_cast<const uint4*>(vc + s_from[r]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kStep;
+            if (r < rows && s_from[r] >= 0 && s_to[r] >= 0) {
+                *reinterpret_cast<uint4*>(kc + s_to[r]) = x[i];
+                *reinterpret_cast<uint4*>(vc + s_to[r]) = y[i];
+            }
+        }
     }
 }
 
@@ -127,24 +281,68 @@ int64_t most_moves(int64_t max_len, int64_t keep) {
     return behind < keep ? behind : keep;
 }
 
+template <int kThreads>
+cudaError_t launch_select(const SelectArgs& s, int cluster, size_t smem, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(s.e.N * s.e.H * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kThreads>, s);
+}
+
+// Blocks of the two launches count in 31 bits.
+bool grids_fit(int64_t N, int64_t H, int64_t most) {
+    const int64_t chunks = (most + kMoveRows - 1) / kMoveRows;
+    return N * H * kMaxCluster <= INT32_MAX && (double)N * H * (chunks > 0 ? chunks : 1) <= INT32_MAX;
+}
+
 }  // namespace
 
 bool cache_evict_workspace(int64_t N, int64_t H, int64_t max_len, int64_t keep, size_t* bytes) {
     const int64_t most = most_moves(max_len, keep);
-    if ((double)N * H * (2.0 * most + 1) * 4 > 9e18) return false;
+    if (!grids_fit(N, H, most)) return false;
     *bytes = (size_t)(N * H) * (size_t)(2 * most + 1) * 4;
     return true;
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     if (a.N == 0) return cudaSuccess;
-    const int row16 = a.d * (a.io == Io::BF16 ? 2 : 4) / 16;
-    const int most = (int)most_moves(a.max_len, a.keep);
-    int* counts = static_cast<int*>(a.workspace);
-    int* lists = counts + (int64_t)a.N * a.H;
-    const unsigned grid = (unsigned)(a.N * a.H);
-    select_kernel<<<grid, kThreads, 0, stream>>>(a, counts, lists, most);
-    move_kernel<<<grid, kThreads, 0, stream>>>(a, counts, lists, most, row16);
+    SelectArgs s;
+    s.e = a;
+    s.most = (int)most_moves(a.max_len, a.keep);
+    s.counts = static_cast<int*>(a.workspace);
+    s.lists = s.counts + (int64_t)a.N * a.H;
+    // a block for up to 8192 slots, 8 at most; below 2048 slots fewer threads meet at the barriers
+    int cluster = 1;
+    while (cluster < kMaxCluster && (int64_t)cluster * 8192 < a.max_len) cluster *= 2;
+    const bool small = a.max_len <= 2048;
+    const int round = cluster * (small ? 256 : 1024);    // a block's slots come in whole rounds
+    const int64_t need = ((int64_t)a.max_len + round - 1) / round * (small ? 256 : 1024);
+    s.keys = need <= kMaxKeys ? (int)need : 0;
+    const size_t smem = (size_t)s.keys * 4;
+    cudaError_t e = small ? launch_select<256>(s, cluster, smem, stream)
+                          : launch_select<1024>(s, cluster, smem, stream);
+    if (e != cudaSuccess) return e;
+    const int esz = a.io == Io::BF16 ? 2 : 4;
+    const int chunks = s.most > 0 ? (s.most + kMoveRows - 1) / kMoveRows : 1;
+    const unsigned grid = (unsigned)((int64_t)a.N * a.H * chunks);
+    switch (a.d * esz / 16) {
+        case 8: evict_move_kernel<8><<<grid, kMoveThreads, 0, stream>>>(s, chunks, esz); break;
+        case 16: evict_move_kernel<16><<<grid, kMoveThreads, 0, stream>>>(s, chunks, esz); break;
+        case 32: evict_move_kernel<32><<<grid, kMoveThreads, 0, stream>>>(s, chunks, esz); break;
+        default: return cudaErrorInvalidValue;
+    }
     return cudaGetLastError();
 }
 
