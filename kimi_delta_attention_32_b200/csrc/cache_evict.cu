@@ -12,7 +12,7 @@
 // Each block reads its part of acc and pos once, into 32-bit keys in shared memory (up to 49152 a
 // block; longer caches are read again in every pass), and all passes run on those: three of a
 // radix select (11, 11 and 10 bits from the top; the blocks' histograms are summed through
-// distributed shared memory), one that counts ties, one that counts what is kept, and one that
+// distributed shared memory), one that counts what lies before each warp's slots, and one that
 // writes the lists of holes and of the entries that fill them. Integers only: no order of
 // atomics can show. It is bound by the latency of its dozen barriers and, for long caches, by
 // shared-memory atomics; the traffic is one read of acc and pos.
@@ -51,34 +51,42 @@ struct SelectArgs {
 template <int kThreads>
 __device__ __forceinline__ int block_scan(int x, int* buf, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int y = x;
+    auto warp_scan = [&](int y) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-    }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        return y;
+    };
+    const int y = warp_scan(x);
     __syncthreads();
     if (lane == 31) buf[warp] = y;
     __syncthreads();
-    int before = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += buf[w];
-        sum += buf[w];
-    }
-    *total = sum;
-    return before + y - x;
+    const int sums = warp_scan(lane < kThreads / 32 ? buf[lane] : 0);      // every warp on its own
+    *total = __shfl_sync(0xffffffffu, sums, 31);
+    const int before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0) + y - x;
 }
 
-template <int kThreads>
+// kMany: the cluster has more than one block.
+template <int kThreads, bool kMany>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs s) {
     extern __shared__ uint32_t s_keys[];
     __shared__ int s_hist[3][kBins];
     __shared__ int s_buf[kThreads / 32], s_pick[2];
-    __shared__ int s_share[2][2];                        // this block's counts, read by the cluster
+    __shared__ int s_share[4];                           // this block's counts, read by the cluster
+    constexpr int kWarps = kThreads / 32, kAhead = 8;    // kAhead: entries a thread loads at once
     const EvictArgs& a = s.e;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    int CS = 1, rank = 0;
+    if constexpr (kMany) {
+        CS = (int)cg::this_cluster().num_blocks();
+        rank = (int)cg::this_cluster().block_rank();
+    }
+    auto sync_all = [&]() {
+        if constexpr (kMany) cg::this_cluster().sync();
+        else __syncthreads();
+    };
     const int64_t nh = blockIdx.x / CS, n = nh / a.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int len = checked_len(a.seqlens[n], a.max_len, a.c.err);
@@ -96,8 +104,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
     }
     // the block's slots [lo, hi), a warp's a contiguous run of whole 32s of them
     const int per_warp = ((len + CS * kThreads - 1) / (CS * kThreads)) * 32;
-    const int lo = min(len, rank * (kThreads / 32) * per_warp);
-    const int hi = min(len, lo + (kThreads / 32) * per_warp);
+    const int lo = min(len, rank * kWarps * per_warp);
+    const int hi = min(len, lo + kWarps * per_warp);
     const bool held = hi - lo <= s.keys;
     auto fresh = [&](int j) { return rank_key(a.acc[at + j], a.pos[at + j], a.n_first, recent_from); };
     auto key = [&](int j) { return held ? s_keys[j - lo] : fresh(j); };
@@ -113,18 +121,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);   // bits found already
-        for (int base = lo; base < hi; base += kThreads) {
-            const int j = base + tid;
-            uint32_t k = 0;
-            bool in = j < hi;
-            if (in) {
-                k = pass == 0 || !held ? fresh(j) : s_keys[j - lo];
-                if (pass == 0 && held) s_keys[j - lo] = k;
-                in = (k & above) == (T & above);
-            }
+        auto count = [&](uint32_t k, bool in) {
+            in = in && (k & above) == (T & above);
             const int digit = (int)(k >> shift) & ((1 << bits) - 1);
             const unsigned who = __ballot_sync(0xffffffffu, in);
-            if (who == 0) continue;
+            if (who == 0) return;
             // one atomic where a warp's keys agree, as in a run of guarded or never-seen entries
             const int lead = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
             if (__all_sync(0xffffffffu, !in || digit == lead)) {
@@ -132,17 +133,51 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
             } else if (in) {
                 atomicAdd(&s_hist[pass][digit], 1);
             }
+        };
+        if (pass == 0) {                                 // the one read of acc and pos
+            for (int base = lo; base < hi; base += kThreads * kAhead) {
+                float w[kAhead];
+                int q[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int j = base + u * kThreads + tid;
+                    w[u] = j < hi ? a.acc[at + j] : 0.f;
+                    q[u] = j < hi ? a.pos[at + j] : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int j = base + u * kThreads + tid;
+                    if (base + u * kThreads >= hi) break;
+                    const uint32_t k = rank_key(w[u], q[u], a.n_first, recent_from);
+                    if (j < hi && held) s_keys[j - lo] = k;
+                    if (j < hi && j < a.keep) {          // a hole's are overwritten by the move
+                        if (copy_acc) a.acc_out[at + j] = w[u];
+                        if (copy_pos) a.pos_out[at + j] = q[u];
+                    }
+                    count(k, j < hi);
+                }
+            }
+        } else {
+            for (int base = lo; base < hi; base += kThreads) {
+                const int j = base + tid;
+                count(j < hi ? key(j) : 0, j < hi);
+            }
         }
-        cluster.sync();
+        sync_all();
         constexpr int kPer = kBins / kThreads;           // bins a thread sums, from the top down
         int c[kPer], mine = 0, total;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int bin = kBins - 1 - (tid * kPer + i);
-            c[i] = 0;
-            for (int r = 0; r < CS; ++r) c[i] += cluster.map_shared_rank(&s_hist[pass][0], r)[bin];
-            mine += c[i];
+        for (int i = 0; i < kPer; ++i) c[i] = 0;
+#pragma unroll
+        for (int r = 0; r < (kMany ? kMaxCluster : 1); ++r) {
+            if (r >= CS) break;
+            const int* hist = s_hist[pass];
+            if constexpr (kMany) hist = cg::this_cluster().map_shared_rank(&s_hist[pass][0], r);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) c[i] += hist[kBins - 1 - (tid * kPer + i)];
         }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) mine += c[i];
         int over = block_scan<kThreads>(mine, s_buf, &total);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -155,69 +190,66 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
         __syncthreads();
         T |= (uint32_t)s_pick[0] << shift;
         left = s_pick[1];
-        __syncthreads();
     }
 
-    // ---- ties: of the entries with key T the `left` lowest slots stay
+    // ---- Of the entries with key T the `left` lowest slots stay, so what is kept before a slot
+    // follows from four counts before it: keys above T and keys equal to T, in front (slots < keep)
+    // and behind. Front slots come first, so the kept ties in front are min(left, ties in front).
     const int w0 = min(hi, lo + warp * per_warp), w1 = min(hi, w0 + per_warp);
-    int ties = 0, total;
-    for (int j0 = w0; j0 < w1; j0 += 32)
-        ties += __popc(__ballot_sync(0xffffffffu, j0 + lane < w1 && key(j0 + lane) == T));
-    int tie_at = block_scan<kThreads>(lane == 0 ? ties : 0, s_buf, &total);
-    if (tid == 0) s_share[0][0] = total;
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) tie_at += cluster.map_shared_rank(&s_share[0][0], r)[0];
-    tie_at = __shfl_sync(0xffffffffu, tie_at, 0);
-
-    // ---- walk the warp's slots: kept or not, in slot order
-    auto walk = [&](auto&& visit) {
-        int seen = tie_at;
-        for (int j0 = w0; j0 < w1; j0 += 32) {
-            const int j = j0 + lane;
-            const uint32_t k = j < w1 ? key(j) : 0;
-            const bool tie = j < w1 && k == T;
-            const unsigned tied = __ballot_sync(0xffffffffu, tie);
-            const bool kept = j < w1 && (k > T || (tie && seen + __popc(tied & ((1u << lane) - 1)) < left));
-            seen += __popc(tied);
-            visit(j, kept);
+    int cnt[4] = {0, 0, 0, 0};                           // above in front, behind; ties in front, behind
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+        const int j = j0 + lane;
+        const uint32_t k = j < w1 ? key(j) : 0;
+        const unsigned up = __ballot_sync(0xffffffffu, j < w1 && k > T);
+        const unsigned tie = __ballot_sync(0xffffffffu, j < w1 && k == T);
+        const unsigned in_front = __ballot_sync(0xffffffffu, j < a.keep);
+        cnt[0] += __popc(up & in_front);
+        cnt[1] += __popc(up & ~in_front);
+        cnt[2] += __popc(tie & in_front);
+        cnt[3] += __popc(tie & ~in_front);
+    }
+    int all[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        cnt[i] = block_scan<kThreads>(lane == 0 ? cnt[i] : 0, s_buf, &all[i]);
+        cnt[i] = __shfl_sync(0xffffffffu, cnt[i], 0);
+    }
+    if constexpr (kMany) {
+        if (tid < 4) s_share[tid] = tid == 0 ? all[0] : tid == 1 ? all[1] : tid == 2 ? all[2] : all[3];
+        cg::this_cluster().sync();
+        for (int r = 0; r < rank; ++r) {
+            const int* share = cg::this_cluster().map_shared_rank(&s_share[0], r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cnt[i] += share[i];
         }
-    };
-    int front = 0, behind = 0;                           // kept in slots < keep, and >= keep
-    walk([&](int j, bool kept) {
-        front += __popc(__ballot_sync(0xffffffffu, kept && j < a.keep));
-        behind += __popc(__ballot_sync(0xffffffffu, kept && j >= a.keep));
-    });
-    int all_front, all_behind;
-    int front_at = block_scan<kThreads>(lane == 0 ? front : 0, s_buf, &all_front);
-    int behind_at = block_scan<kThreads>(lane == 0 ? behind : 0, s_buf, &all_behind);
-    if (tid == 0) {
-        s_share[1][0] = all_front;
-        s_share[1][1] = all_behind;
     }
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-        front_at += cluster.map_shared_rank(&s_share[1][0], r)[0];
-        behind_at += cluster.map_shared_rank(&s_share[1][0], r)[1];
-    }
-    front_at = __shfl_sync(0xffffffffu, front_at, 0);
-    behind_at = __shfl_sync(0xffffffffu, behind_at, 0);
     int* hole = s.lists + nh * 2 * s.most;
     int* tail = hole + s.most;
-    walk([&](int j, bool kept) {
-        const unsigned f = __ballot_sync(0xffffffffu, kept && j < a.keep);
-        const unsigned t = __ballot_sync(0xffffffffu, kept && j >= a.keep);
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+        const int j = j0 + lane;
+        const uint32_t k = j < w1 ? key(j) : 0;
+        const unsigned up = __ballot_sync(0xffffffffu, j < w1 && k > T);
+        const unsigned tie = __ballot_sync(0xffffffffu, j < w1 && k == T);
+        const unsigned in_front = __ballot_sync(0xffffffffu, j < a.keep);
         const unsigned before = (1u << lane) - 1;
-        if (j < w1 && j < a.keep && !kept) hole[j - (front_at + __popc(f & before))] = j;
-        if (kept && j >= a.keep) tail[behind_at + __popc(t & before)] = j;
-        if (kept && j < a.keep) {
-            if (copy_acc) a.acc_out[at + j] = a.acc[at + j];
-            if (copy_pos) a.pos_out[at + j] = a.pos[at + j];
+        // counts before slot j
+        const int up_f = cnt[0] + __popc(up & in_front & before), up_b = cnt[1] + __popc(up & ~in_front & before);
+        const int tie_f = cnt[2] + __popc(tie & in_front & before), tie_b = cnt[3] + __popc(tie & ~in_front & before);
+        const int stay_f = min(left, tie_f), stay_b = min(left, tie_f + tie_b) - stay_f;
+        const bool kept = (up >> lane & 1) || ((tie >> lane & 1) && tie_f + tie_b < left);
+        if (j < w1) {
+            if (j < a.keep && !kept) hole[j - (up_f + stay_f)] = j;
+            if (j >= a.keep && kept) tail[up_b + stay_b] = j;
         }
-        front_at += __popc(f);
-        behind_at += __popc(t);
-    });
-    if (rank == CS - 1 && tid == kThreads - 1) s.counts[nh] = behind_at;      // the last warp's end: all
-    cluster.sync();                                      // shared memory stays until all have read it
+        cnt[0] += __popc(up & in_front);
+        cnt[1] += __popc(up & ~in_front);
+        cnt[2] += __popc(tie & in_front);
+        cnt[3] += __popc(tie & ~in_front);
+    }
+    // after the last warp's slots: all that is kept behind keep
+    if (rank == CS - 1 && tid == kThreads - 1)
+        s.counts[nh] = cnt[1] + min(left, cnt[2] + cnt[3]) - min(left, cnt[2]);
+    if constexpr (kMany) cg::this_cluster().sync();      // shared memory stays until all have read it
 }
 
 constexpr int kMoveThreads = 256, kMoveRows = 64;
@@ -281,10 +313,10 @@ int64_t most_moves(int64_t max_len, int64_t keep) {
     return behind < keep ? behind : keep;
 }
 
-template <int kThreads>
+template <int kThreads, bool kMany>
 cudaError_t launch_select(const SelectArgs& s, int cluster, size_t smem, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto kernel = evict_select_kernel<kThreads, kMany>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(s.e.N * s.e.H * cluster));
@@ -297,8 +329,8 @@ cudaError_t launch_select(const SelectArgs& s, int cluster, size_t smem, cudaStr
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kThreads>, s);
+    cfg.numAttrs = kMany ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, s);
 }
 
 // Blocks of the two launches count in 31 bits.
@@ -331,8 +363,9 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     const int64_t need = ((int64_t)a.max_len + round - 1) / round * (small ? 256 : 1024);
     s.keys = need <= kMaxKeys ? (int)need : 0;
     const size_t smem = (size_t)s.keys * 4;
-    cudaError_t e = small ? launch_select<256>(s, cluster, smem, stream)
-                          : launch_select<1024>(s, cluster, smem, stream);
+    cudaError_t e = small         ? launch_select<256, false>(s, 1, smem, stream)
+                    : cluster > 1 ? launch_select<1024, true>(s, cluster, smem, stream)
+                                  : launch_select<1024, false>(s, 1, smem, stream);
     if (e != cudaSuccess) return e;
     const int esz = a.io == Io::BF16 ? 2 : 4;
     const int chunks = s.most > 0 ? (s.most + kMoveRows - 1) / kMoveRows : 1;
