@@ -98,6 +98,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Programmatic dependent launch: a kernel launched with launch_after may start while the one before
+// it on the stream ends; it waits here until that one has finished and its writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
 // Sizes of one instantiation. NT: tiles of 8 query heads that a block works on at once.
@@ -549,49 +553,55 @@ paged_decode_kernel(const Params p) {
         if (i + 1 < count) next(cur);
     }
     cp_wait<0>();
+    grid_release();
 }
 
 // Joins the parts of the segment that begins in block blockIdx.x and goes on in later ones.
 // blockIdx.y: eight of the part's registers (two blocks of 16 channels of one tile of 8 heads).
-constexpr int kJoinWarps = 4;
+// A long sequence alone leaves a hundred parts to one head: its warps take every eighth part, four
+// at a time.
+constexpr int kJoinWarps = 8;
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Params p) {
     using X = Shape<T, D, NT>;
-    __shared__ float s_f[kMaxBlocks][8];
+    __shared__ float s_f[kMaxBlocks][8], s_l[kMaxBlocks][8];
     __shared__ float s_sum[8], s_top[8];
     __shared__ float s_o[kJoinWarps][8][32];
+    grid_wait();
     const int b = blockIdx.x, r0 = blockIdx.y * 8, nt = r0 / (D / 4);
-    const int last = p.meta[4 * b + 2];
-    if (last < 0) return;
-    const int n = p.meta[4 * b], head = p.meta[4 * b + 1], k = last - b + 1;
+    const int4 meta = *reinterpret_cast<const int4*>(p.meta + 4 * b);
+    if (meta.z < 0) return;
+    const int n = meta.x, head = meta.y, k = meta.z - b + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto part = [&](int j) { return p.parts + (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * X::kPart; };
-    for (int e = tid; e < k * 8; e += kJoinWarps * 32)
-        s_f[e >> 3][e & 7] = part(e >> 3)[X::kRegs * 32 + nt * 8 + (e & 7)];
+    for (int e = tid; e < k * 8; e += kJoinWarps * 32) {
+        const float* ml = part(e >> 3) + X::kRegs * 32 + nt * 8 + (e & 7);
+        s_f[e >> 3][e & 7] = ml[0];
+        s_l[e >> 3][e & 7] = ml[8 * NT];
+    }
     __syncthreads();
-    {                                          // 16 threads a head: the maximum, then factors and sum
-        const int h = tid >> 4, u = tid & 15;
+    {                                          // a warp a head: the maximum, then factors and sum
         float mx = -INFINITY, sm = 0.f;
-        for (int j = u; j < k; j += 16) mx = fmaxf(mx, s_f[j][h]);
+        for (int j = lane; j < k; j += 32) mx = fmaxf(mx, s_f[j][warp]);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const float base = mx == -INFINITY ? 0.f : mx;
-        for (int j = u; j < k; j += 16) {
-            const float f = exp2_fast(s_f[j][h] - base);
-            s_f[j][h] = f;
-            sm += f * part(j)[X::kRegs * 32 + 8 * NT + nt * 8 + h];
+        for (int j = lane; j < k; j += 32) {
+            const float f = exp2_fast(s_f[j][warp] - base);
+            s_f[j][warp] = f;
+            sm += f * s_l[j][warp];
         }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sm += __shfl_xor_sync(0xffffffffu, sm, o);
-        if (u == 0) {
-            s_sum[h] = sm;
-            s_top[h] = base;
+        sm = warp_sum(sm);
+        if (lane == 0) {
+            s_sum[warp] = sm;
+            s_top[warp] = base;
         }
     }
     __syncthreads();
     float y[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) y[r] = 0.f;
+#pragma unroll 4
     for (int j = warp; j < k; j += kJoinWarps) {
         const float* src = part(j) + r0 * 32 + lane;
         const float f0 = s_f[j][2 * (lane & 3)], f1 = s_f[j][2 * (lane & 3) + 1];
@@ -602,15 +612,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Param
     for (int r = 0; r < 8; ++r) s_o[warp][r][lane] = y[r];
     __syncthreads();
     const int g0 = head / p.GT * p.G, first = (head % p.GT) * 8 * NT;
+    static_assert(kJoinWarps == 8, "a warp a register and a head");
+    float v = 0.f;
 #pragma unroll
-    for (int u = 0; u < 8 / kJoinWarps; ++u) {
-        const int r = warp * (8 / kJoinWarps) + u;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) v += s_o[w][r][lane];
-        int h, ch;
-        part_coord<D>(r0 + r, lane, h, ch);
-        if (first + h >= p.G) continue;
+    for (int w = 0; w < kJoinWarps; ++w) v += s_o[w][warp][lane];
+    int h, ch;
+    part_coord<D>(r0 + warp, lane, h, ch);
+    if (first + h < p.G) {
         const float sm = s_sum[h & 7];
         v = sm > 0.f ? v / sm : 0.f;
         const int64_t at = ((int64_t)n * p.Hq + g0 + first + h) * D + ch;
@@ -622,30 +630,42 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Param
             make_float2(s_top[tid], s_sum[tid] > 0.f ? 1.f / s_sum[tid] : 0.f);
 }
 
-// acc[n, h, j] += sum over the group's heads of exp2(score - max) / sum.
-constexpr int kWeightThreads = 128;
+// acc[n, h, j] += sum over the group's heads of exp2(score - max) / sum. Four slots a thread.
+constexpr int kWeightThreads = 128, kWeightSlots = 4 * kWeightThreads;
 template <int kTile>
 __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(const Params p, int NT8) {
-    const int chunks = (p.max_len + kWeightThreads - 1) / kWeightThreads;
+    grid_wait();
+    const int chunks = (p.max_len + kWeightSlots - 1) / kWeightSlots;
     const int64_t all = (int64_t)p.N * p.H * chunks;
     for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
         const int64_t nh = w / chunks, n = nh / p.H;
-        const int j = (int)(w % chunks) * kWeightThreads + threadIdx.x, h = (int)(nh % p.H);
+        const int j = (int)(w % chunks) * kWeightSlots + threadIdx.x * 4, h = (int)(nh % p.H);
         const int len = checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err);
+        const int64_t before = p.tiles_before[n];
         if (j >= len) continue;
+        float* acc = p.acc + nh * p.slots + j;
+        float old[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) old[u] = j + u < len ? acc[u] : 0.f;
         const int tiles = (len + kTile - 1) / kTile;
-        const int64_t tile = ((int64_t)p.tiles_before[n] * p.H + (int64_t)h * tiles) * p.GT + j / kTile;
+        const int64_t tile = (before * p.H + (int64_t)h * tiles) * p.GT + j / kTile;
         const float2* st = p.stats + n * p.Hq + h * p.G;
-        float sum = 0.f;
         for (int gt = 0; gt < p.GT; ++gt) {
             const float* s = p.scores + (tile + (int64_t)gt * tiles) * p.GS * kTile + j % kTile;
             const int gs = min(NT8, p.G - gt * NT8);
+#pragma unroll 4
             for (int g = 0; g < gs; ++g) {
                 const float2 t = st[gt * NT8 + g];
-                sum = fmaf(exp2_fast(s[g * kTile] - t.x), t.y, sum);
+                const float4 x = *reinterpret_cast<const float4*>(s + g * kTile);
+                sum[0] = fmaf(exp2_fast(x.x - t.x), t.y, sum[0]);
+                sum[1] = fmaf(exp2_fast(x.y - t.x), t.y, sum[1]);
+                sum[2] = fmaf(exp2_fast(x.z - t.x), t.y, sum[2]);
+                sum[3] = fmaf(exp2_fast(x.w - t.x), t.y, sum[3]);
             }
         }
-        p.acc[nh * p.slots + j] += sum;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < len) acc[u] = old[u] + sum[u];
     }
 }
 
@@ -678,6 +698,21 @@ int sm_count() {
     return n;
 }
 
+// Launches a kernel that begins with grid_wait().
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 template <typename T, int D, int NT>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     using X = Shape<T, D, NT>;
@@ -708,13 +743,13 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X::kSmem);
     if (e != cudaSuccess) return e;
     paged_decode_kernel<T, D, NT><<<p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
-    paged_join_kernel<T, D, NT><<<dim3(p.most_blocks, X::kRegs / 8), kJoinWarps * 32, 0, stream>>>(p);
-    if (a.acc != nullptr && a.max_len > 0) {
-        const int64_t all = (int64_t)a.N * a.H * ((a.max_len + kWeightThreads - 1) / kWeightThreads);
-        const unsigned grid = (unsigned)(all < sms * 16 ? all : sms * 16);
-        paged_weights_kernel<X::kTile><<<grid, kWeightThreads, 0, stream>>>(p, 8 * NT);
-    }
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(paged_join_kernel<T, D, NT>, dim3(p.most_blocks, X::kRegs / 8), kJoinWarps * 32,
+                     stream, p);
+    if (e != cudaSuccess || a.acc == nullptr || a.max_len == 0) return e;
+    const int64_t all = (int64_t)a.N * a.H * ((a.max_len + kWeightSlots - 1) / kWeightSlots);
+    const unsigned grid = (unsigned)(all < sms * 16 ? all : sms * 16);
+    return launch_after(paged_weights_kernel<X::kTile>, dim3(grid), kWeightThreads, stream, p, 8 * NT);
 }
 
 template <typename T, int D>
