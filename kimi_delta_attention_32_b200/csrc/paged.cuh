@@ -3,6 +3,8 @@
 
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "launchers.h"
 
@@ -27,6 +29,20 @@ __device__ __forceinline__ int64_t slot_offset(const PagedCache& c, int64_t n, i
         return -1;
     }
     return page * c.page_stride + (slot % c.page_size) * c.slot_stride;
+}
+
+// Raises a kernel's limit of dynamic shared memory, once per device: `done` (one per kernel) has a
+// bit for each of the first 64 devices.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 }  // namespace kda

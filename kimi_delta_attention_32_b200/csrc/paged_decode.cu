@@ -690,11 +690,14 @@ Layout layout(int64_t N, int64_t Hq, int64_t H, int64_t max_len, bool with_acc, 
     return l;
 }
 
+// SMs of the current device (0 if the query fails); cached per device.
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -739,8 +742,8 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     p.GS = p.G < 8 * NT ? p.G : 8 * NT;
     p.acc = a.acc;
     p.slots = a.slots;
-    cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<T, D, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X::kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(paged_decode_kernel<T, D, NT>, X::kSmem, allowed);
     if (e != cudaSuccess) return e;
     paged_decode_kernel<T, D, NT><<<p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

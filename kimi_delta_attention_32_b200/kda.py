@@ -431,11 +431,12 @@ def fused_recurrent_step(q_raw, k_raw, v_raw, g_raw, beta_raw, w_q, w_k, w_v, co
     return o
 
 
-def _need(name, t, dtype, shape, device, none_ok=False):
-    """t is a dense tensor of this dtype and shape on this device (or None where that is allowed)."""
+# The paged cache's calls run once a layer and decoded token, on small inputs: their checks pass
+# good arguments with few operations and leave the reasons of bad ones to _refuse. The callers keep
+# their tensors' names bound to the end: an address alone does not keep its memory.
+
+def _refuse(name, t, dtype, shape, device):
     if t is None:
-        if none_ok:
-            return
         raise TypeError(f"{name} is required")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -443,39 +444,59 @@ def _need(name, t, dtype, shape, device, none_ok=False):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    raise ValueError(f"{name} is on {t.device}, the cache on device {device}")
+
+
+def _need(name, t, dtype, shape, device):
+    """The address of t: a dense tensor of this dtype and shape on this device (its index)."""
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or \
+            t.get_device() != device:
+        _refuse(name, t, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _may(name, t, dtype, shape, device):
+    return None if t is None else _need(name, t, dtype, shape, device)
+
+
+_IO = {torch.bfloat16: KDA_IO_BF16, torch.float32: KDA_IO_F32}
 
 
 def _paged(k_cache, v_cache, block_table, seqlens):
-    """Checks the cache tensors; returns (C arguments up to max_pages, N, page_size, Hkv, d)."""
-    _io(k_cache)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or \
-            k_cache.device != v_cache.device or block_table.dim() != 2:
+    """Checks the cache tensors. Returns (C arguments from k_cache to seqlens), and N, page_size,
+    Hkv, d, dtype, C io, device index."""
+    dtype, dev = k_cache.dtype, k_cache.get_device()
+    io = _IO.get(dtype)
+    if io is None:
+        raise TypeError(f"unsupported I/O dtype {dtype}")
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype or \
+            v_cache.get_device() != dev or block_table.dim() != 2:
         raise ValueError("k_cache and v_cache: two [pages, page_size, Hkv, d] tensors of one dtype "
                          "and device; block_table: [N, max_pages]")
-    dev = k_cache.device
-    pages, page_size, H, d = k_cache.shape
-    # strides; that of a dimension of size 1 is never used
-    sk, sv = ([st if n > 1 else d for n, st in zip(t.shape[:3], t.stride())]
-              for t in (k_cache, v_cache))
-    if sk != sv or (d > 1 and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1)):
+    pages, page_size, H, d = shape
+    sv = v_cache.stride()
+    if 1 in shape:              # the stride of a dimension of size 1 is never used
+        st, sv = ([x if n > 1 else y for n, x, y in zip(shape, u, (d, d, d, 1))] for u in (st, sv))
+    if st != sv or st[3] != 1:
         raise ValueError("k_cache and v_cache need the same strides, with the last dimension dense")
     N, max_pages = block_table.shape
-    _need("block_table", block_table, torch.int32, (N, max_pages), dev)
-    _need("seqlens", seqlens, torch.int32, (N,), dev)
-    return (_ptr(k_cache), _ptr(v_cache), *sk, pages, page_size, _ptr(block_table),
-            max_pages), N, page_size, H, d
+    args = (k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], pages, page_size,
+            _need("block_table", block_table, torch.int32, (N, max_pages), dev), max_pages,
+            _need("seqlens", seqlens, torch.int32, (N,), dev))
+    return args, N, page_size, H, d, dtype, io, dev
 
 
-def _call_on(device, stream, fn, *args):
+def _call_on(dev, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
-    if device.type != "cuda":
-        raise ValueError(f"the cache must be a CUDA tensor, not {device}")
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
-    with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+    if dev < 0:
+        raise ValueError("the cache must be a CUDA tensor")
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _call_on(dev, stream, fn, *args)
+    if stream is None:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    return fn(*args, _stream(stream))
 
 
 def cache_append(k, v, k_cache, v_cache, block_table, seqlens, positions=None, acc=None, pos=None,
@@ -486,41 +507,37 @@ def cache_append(k, v, k_cache, v_cache, block_table, seqlens, positions=None, a
     dense); block_table [N,max_pages], seqlens and positions [N], int32; acc (fp32) and pos
     (int32) [N,Hkv,slots], whose new entries become 0 and positions[n] + i (seqlens[n] + i without
     positions). seqlens and positions are not advanced."""
-    lib = load_library()
-    cache, N, _, H, d = _paged(k_cache, v_cache, block_table, seqlens)
-    dev = k_cache.device
+    lib = _lib or load_library()
+    cache, N, _, H, d, dtype, io, dev = _paged(k_cache, v_cache, block_table, seqlens)
+    cu, keep, cuh = None, None, None
     if cu_seqlens is None:
         if k.dim() != 4:
             raise ValueError("without cu_seqlens k is [B, T, Hkv, d]")
-        B, T = k.shape[:2]
+        B, T = k.shape[0], k.shape[1]
         if B != N:
             raise ValueError(f"k has {B} sequences, block_table {N}")
         shape = (B, T, H, d)
     else:
         B, T = 1, 0
-        _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
+        cu = _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
         if cu_host is None or len(cu_host) != N + 1:
             raise ValueError("cu_host must hold the values of cu_seqlens")
-        shape = (int(cu_host[N]), H, d)
-    _need("k", k, k_cache.dtype, shape, dev)
-    _need("v", v, k_cache.dtype, shape, dev)
-    _need("positions", positions, torch.int32, (N,), dev, none_ok=True)
-    side = acc if acc is not None else pos
-    slots = 0
-    if side is not None:
-        slots = side.shape[-1]
-        _need("acc", acc, torch.float32, (N, H, slots), dev, none_ok=True)
-        _need("pos", pos, torch.int32, (N, H, slots), dev, none_ok=True)
-        if slots == 0 and k.numel():
-            raise ValueError("acc and pos have no slots")
+        keep, cuh = _host_cu(cu_host)
+        shape = (keep[N], H, d)
+    k_p, v_p = _need("k", k, dtype, shape, dev), _need("v", v, dtype, shape, dev)
+    seen_p = _may("positions", positions, torch.int32, (N,), dev)
+    slots = acc.shape[-1] if acc is not None else pos.shape[-1] if pos is not None else 0
+    acc_p = _may("acc", acc, torch.float32, (N, H, slots), dev)
+    pos_p = _may("pos", pos, torch.int32, (N, H, slots), dev)
     if k.numel() == 0:
         return
-    keep, cuh = _host_cu(cu_host if cu_seqlens is not None else None)
-    st = _call_on(dev, stream, lib.kda_cache_append, _ptr(k), _ptr(v), *cache, _ptr(seqlens),
-                  _ptr(positions), _ptr(acc), _ptr(pos), slots, _ptr(cu_seqlens), cuh, B, T, N, H,
-                  d, _io(k_cache))
+    if slots == 0 and (acc is not None or pos is not None):
+        raise ValueError("acc and pos have no slots")
+    st = _call_on(dev, stream, lib.kda_cache_append, k_p, v_p, *cache, seen_p, acc_p, pos_p, slots,
+                  cu, cuh, B, T, N, H, d, io)
     del keep
-    _check("kda_cache_append", st)
+    if st:
+        _check("kda_cache_append", st)
 
 
 def paged_decode_workspace_size(N, Hq, Hkv, d, max_len, with_acc=False) -> int:
@@ -532,12 +549,12 @@ def paged_decode_workspace_size(N, Hq, Hkv, d, max_len, with_acc=False) -> int:
     return out.value
 
 
-def _workspace(workspace, need, device):
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+def _workspace(workspace, device):
+    """(address, bytes) of the caller's workspace."""
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or \
+            workspace.get_device() != device:
         raise ValueError("workspace: a contiguous uint8 tensor on the cache's device")
-    return workspace
+    return workspace.data_ptr(), workspace.numel()
 
 
 def paged_decode(q, k_cache, v_cache, block_table, seqlens, scale=1.0, z=None, acc=None,
@@ -547,37 +564,33 @@ def paged_decode(q, k_cache, v_cache, block_table, seqlens, scale=1.0, z=None, a
     sigmoid(z) when z [N,Hq,d] is given. acc [N,Hkv,slots] fp32 gathers the weights, summed over
     the query heads of each key-value head. max_len: host bound on seqlens (default: what
     block_table can hold, or acc's slots). Returns o [N,Hq,d]."""
-    lib = load_library()
-    cache, N, page_size, H, d = _paged(k_cache, v_cache, block_table, seqlens)
-    dev = k_cache.device
+    lib = _lib or load_library()
+    cache, N, page_size, H, d, dtype, io, dev = _paged(k_cache, v_cache, block_table, seqlens)
     if q.dim() != 3:
         raise ValueError("q is [N, Hq, d]")
     Hq = q.shape[1]
-    _need("q", q, k_cache.dtype, (N, Hq, d), dev)
-    _need("z", z, k_cache.dtype, (N, Hq, d), dev, none_ok=True)
+    shape = (N, Hq, d)
+    q_p = _need("q", q, dtype, shape, dev)
+    z_p = _may("z", z, dtype, shape, dev)
     if o is None:
         o = torch.empty_like(q)
-    else:
-        _need("o", o, k_cache.dtype, (N, Hq, d), dev)
-    slots = 0
-    if acc is not None:
-        slots = acc.shape[-1]
-        _need("acc", acc, torch.float32, (N, H, slots), dev)
+    o_p = _need("o", o, dtype, shape, dev)
+    slots = acc.shape[-1] if acc is not None else 0
+    acc_p = _may("acc", acc, torch.float32, (N, H, slots), dev)
     if N == 0:
         return o
     if max_len is None:
-        max_len = block_table.shape[1] * page_size
+        max_len = cache[8] * page_size
         if acc is not None:
             max_len = min(max_len, slots)
-    if workspace is None:
-        workspace = _workspace(None, paged_decode_workspace_size(N, Hq, H, d, max_len,
-                                                                 acc is not None), dev)
-    else:
-        workspace = _workspace(workspace, 0, dev)
-    st = _call_on(dev, stream, lib.kda_paged_decode, _ptr(q), *cache, _ptr(seqlens), _ptr(z),
-                  float(scale), _ptr(acc), slots, _ptr(o), N, Hq, H, d, max_len, _io(q),
-                  _ptr(workspace), 0 if workspace is None else workspace.numel())
-    _check("kda_paged_decode", st)
+    if workspace is None and dev >= 0:
+        workspace = torch.empty(paged_decode_workspace_size(N, Hq, H, d, max_len, acc is not None),
+                                dtype=torch.uint8, device=q.device)
+    ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (None, 0)
+    st = _call_on(dev, stream, lib.kda_paged_decode, q_p, *cache, z_p, scale, acc_p, slots, o_p, N,
+                  Hq, H, d, max_len, io, ws, ws_bytes)
+    if st:
+        _check("kda_paged_decode", st)
     return o
 
 
@@ -596,34 +609,30 @@ def cache_evict(k_cache, v_cache, block_table, seqlens, keep, acc, pos, position
     with pos < n_first or pos >= positions[n] - n_recent stay before all others. Kept entries
     behind slot keep move into the slots that became free (K and V in place; acc and pos into
     acc_out and pos_out, by default in place too). Returns the new lengths (seqlens_out)."""
-    lib = load_library()
-    cache, N, page_size, H, d = _paged(k_cache, v_cache, block_table, seqlens)
-    dev = k_cache.device
-    _need("acc", acc, torch.float32, (N, H, acc.shape[-1]), dev)
-    slots = acc.shape[-1]
-    _need("pos", pos, torch.int32, (N, H, slots), dev)
-    _need("positions", positions, torch.int32, (N,), dev, none_ok=True)
-    acc_out = acc if acc_out is None else acc_out
-    pos_out = pos if pos_out is None else pos_out
-    _need("acc_out", acc_out, torch.float32, (N, H, slots), dev)
-    _need("pos_out", pos_out, torch.int32, (N, H, slots), dev)
+    lib = _lib or load_library()
+    cache, N, page_size, H, d, _, io, dev = _paged(k_cache, v_cache, block_table, seqlens)
+    slots = acc.shape[-1] if acc is not None else 0
+    shape = (N, H, slots)
+    acc_p = _need("acc", acc, torch.float32, shape, dev)
+    pos_p = _need("pos", pos, torch.int32, shape, dev)
+    seen_p = _may("positions", positions, torch.int32, (N,), dev)
+    ao_p = acc_p if acc_out is None else _need("acc_out", acc_out, torch.float32, shape, dev)
+    po_p = pos_p if pos_out is None else _need("pos_out", pos_out, torch.int32, shape, dev)
     if seqlens_out is None:
         seqlens_out = torch.empty_like(seqlens)
-    else:
-        _need("seqlens_out", seqlens_out, torch.int32, (N,), dev)
+    out_p = _need("seqlens_out", seqlens_out, torch.int32, (N,), dev)
     if N == 0:
         return seqlens_out
     if max_len is None:
-        max_len = min(block_table.shape[1] * page_size, slots)
-    if workspace is None:
-        workspace = _workspace(None, cache_evict_workspace_size(N, H, max_len, keep), dev)
-    else:
-        workspace = _workspace(workspace, 0, dev)
-    st = _call_on(dev, stream, lib.kda_cache_evict, *cache, _ptr(seqlens), _ptr(positions), keep,
-                  n_first, n_recent, _ptr(acc), _ptr(pos), _ptr(acc_out), _ptr(pos_out), slots,
-                  _ptr(seqlens_out), N, H, d, max_len, _io(k_cache), _ptr(workspace),
-                  0 if workspace is None else workspace.numel())
-    _check("kda_cache_evict", st)
+        max_len = min(cache[8] * page_size, slots)
+    if workspace is None and dev >= 0:
+        workspace = torch.empty(cache_evict_workspace_size(N, H, max_len, keep), dtype=torch.uint8,
+                                device=seqlens.device)
+    ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (None, 0)
+    st = _call_on(dev, stream, lib.kda_cache_evict, *cache, seen_p, keep, n_first, n_recent, acc_p,
+                  pos_p, ao_p, po_p, slots, out_p, N, H, d, max_len, io, ws, ws_bytes)
+    if st:
+        _check("kda_cache_evict", st)
     return seqlens_out
 
 
