@@ -556,78 +556,169 @@ paged_decode_kernel(const Params p) {
     grid_release();
 }
 
-// Joins the parts of the segment that begins in block blockIdx.x and goes on in later ones.
-// blockIdx.y: eight of the part's registers (two blocks of 16 channels of one tile of 8 heads).
-// A long sequence alone leaves a hundred parts to one head: its warps take every eighth part, four
-// at a time.
-constexpr int kJoinWarps = 8;
+// Joins the parts of every segment that spans blocks, by two kinds of work items:
+//  - up to kFew parts (many segments then): a segment; each of eight warps takes an eighth of the
+//    output registers through all parts;
+//  - more parts (one long sequence leaves a hundred to each of its heads): two registers of a
+//    segment; the warps take every eighth part. 148 parts of 2 heads: 18.6 us with items of eight
+//    registers, 9.8 us with these.
+constexpr int kJoinWarps = 8, kJoinPerSm = 4, kFew = 8;
+template <int NT>
+struct JoinShared {
+    float f[kMaxBlocks][8], l[kMaxBlocks][8];
+    float few[kFew][8 * NT];
+    float sum[8], top[8];
+    float o[kJoinWarps][2][32];
+    int list[kMaxBlocks], count[2][kJoinWarps];
+};
+
+// The output of head h, channel ch of a segment (h of its head tile), from the weighted sum.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Params p) {
+__device__ __forceinline__ void store_joined(const Params& p, int n, int head, int h, int ch, float v) {
+    const int hg = (head % p.GT) * 8 * NT + h;
+    if (hg >= p.G) return;
+    const int64_t at = ((int64_t)n * p.Hq + head / p.GT * p.G + hg) * D + ch;
+    if (p.z != nullptr) v *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
+    static_cast<T*>(p.o)[at] = from_f32<T>(v);
+}
+template <int NT>
+__device__ __forceinline__ void store_stats(const Params& p, int n, int head, int h, float top, float inv) {
+    const int hg = (head % p.GT) * 8 * NT + h;
+    if (p.stats != nullptr && hg < p.G)
+        p.stats[(int64_t)n * p.Hq + head / p.GT * p.G + hg] = make_float2(top, inv);
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel(const Params p) {
     using X = Shape<T, D, NT>;
-    __shared__ float s_f[kMaxBlocks][8], s_l[kMaxBlocks][8];
-    __shared__ float s_sum[8], s_top[8];
-    __shared__ float s_o[kJoinWarps][8][32];
-    grid_wait();
-    const int b = blockIdx.x, r0 = blockIdx.y * 8, nt = r0 / (D / 4);
-    const int4 meta = *reinterpret_cast<const int4*>(p.meta + 4 * b);
-    if (meta.z < 0) return;
-    const int n = meta.x, head = meta.y, k = meta.z - b + 1;
+    constexpr int kThreads = kJoinWarps * 32, kShare = X::kRegs / kJoinWarps, kPairs = X::kRegs / 2;
+    __shared__ JoinShared<NT> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    auto part = [&](int j) { return p.parts + (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * X::kPart; };
-    for (int e = tid; e < k * 8; e += kJoinWarps * 32) {
-        const float* ml = part(e >> 3) + X::kRegs * 32 + nt * 8 + (e & 7);
-        s_f[e >> 3][e & 7] = ml[0];
-        s_l[e >> 3][e & 7] = ml[8 * NT];
-    }
-    __syncthreads();
-    {                                          // a warp a head: the maximum, then factors and sum
-        float mx = -INFINITY, sm = 0.f;
-        for (int j = lane; j < k; j += 32) mx = fmaxf(mx, s_f[j][warp]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float base = mx == -INFINITY ? 0.f : mx;
-        for (int j = lane; j < k; j += 32) {
-            const float f = exp2_fast(s_f[j][warp] - base);
-            s_f[j][warp] = f;
-            sm += f * s_l[j][warp];
-        }
-        sm = warp_sum(sm);
+    grid_wait();
+    // the blocks whose last segment goes on: those of few parts from the list's start, of many
+    // from its end
+    int few = 0, many = 0;
+    for (int b0 = 0; b0 < p.most_blocks; b0 += kThreads) {
+        const int b = b0 + tid;
+        const int last = b < p.most_blocks ? p.meta[4 * b + 2] : -1;
+        const bool is_few = last >= 0 && last - b + 1 <= kFew, is_many = last >= 0 && !is_few;
+        const unsigned mf = __ballot_sync(0xffffffffu, is_few), mm = __ballot_sync(0xffffffffu, is_many);
         if (lane == 0) {
-            s_sum[warp] = sm;
-            s_top[warp] = base;
+            sh.count[0][warp] = __popc(mf);
+            sh.count[1][warp] = __popc(mm);
         }
+        __syncthreads();
+        int at_few = few + __popc(mf & ((1u << lane) - 1)), at_many = many + __popc(mm & ((1u << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (w < warp) {
+                at_few += sh.count[0][w];
+                at_many += sh.count[1][w];
+            }
+            few += sh.count[0][w];
+            many += sh.count[1][w];
+        }
+        if (is_few) sh.list[at_few] = b;
+        if (is_many) sh.list[kMaxBlocks - 1 - at_many] = b;
+        __syncthreads();
     }
-    __syncthreads();
-    float y[8];
+    auto part = [&](int b, int j) { return p.parts + (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * X::kPart; };
+
+    for (int w = blockIdx.x; w < few + many * kPairs; w += gridDim.x) {
+        const bool pair = w < many * kPairs;
+        const int b = pair ? sh.list[kMaxBlocks - 1 - w / kPairs] : sh.list[w - many * kPairs];
+        const int4 meta = *reinterpret_cast<const int4*>(p.meta + 4 * b);
+        const int n = meta.x, head = meta.y, k = meta.z - b + 1;
+        __syncthreads();                       // the item before has been read
+        if (!pair) {
+            if (tid < 8 * NT) {                // factors exp2(m - max) / sum of each part
+                float m[kFew], l[kFew], mx = -INFINITY, sm = 0.f;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) y[r] = 0.f;
-#pragma unroll 4
-    for (int j = warp; j < k; j += kJoinWarps) {
-        const float* src = part(j) + r0 * 32 + lane;
-        const float f0 = s_f[j][2 * (lane & 3)], f1 = s_f[j][2 * (lane & 3) + 1];
+                for (int j = 0; j < kFew; ++j) {
+                    m[j] = j < k ? part(b, j)[X::kRegs * 32 + tid] : -INFINITY;
+                    l[j] = j < k ? part(b, j)[X::kRegs * 32 + 8 * NT + tid] : 0.f;
+                    mx = fmaxf(mx, m[j]);
+                }
+                const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) y[r] += src[r * 32] * (r & 1 ? f1 : f0);
+                for (int j = 0; j < kFew; ++j) {
+                    m[j] = exp2_fast(m[j] - base);
+                    sm += m[j] * l[j];
+                }
+                const float inv = sm > 0.f ? 1.f / sm : 0.f;
+#pragma unroll
+                for (int j = 0; j < kFew; ++j) sh.few[j][tid] = m[j] * inv;
+                store_stats<NT>(p, n, head, tid, base, inv);
+            }
+            float x[kShare], y[kShare];
+#pragma unroll
+            for (int r = 0; r < kShare; ++r) y[r] = 0.f;
+            __syncthreads();
+#pragma unroll 2
+            for (int j = 0; j < k; ++j) {
+                const float* src = part(b, j) + warp * kShare * 32 + lane;
+#pragma unroll
+                for (int r = 0; r < kShare; ++r) x[r] = src[r * 32];
+#pragma unroll
+                for (int r = 0; r < kShare; ++r) {
+                    int h, ch;
+                    part_coord<D>(warp * kShare + r, lane, h, ch);
+                    y[r] += x[r] * sh.few[j][h];
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < kShare; ++r) {
+                int h, ch;
+                part_coord<D>(warp * kShare + r, lane, h, ch);
+                store_joined<T, D, NT>(p, n, head, h, ch, y[r]);
+            }
+            continue;
+        }
+        const int r0 = w % kPairs * 2, nt = r0 / (D / 4);
+        for (int e = tid; e < k * 8; e += kThreads) {
+            const float* ml = part(b, e >> 3) + X::kRegs * 32 + nt * 8 + (e & 7);
+            sh.f[e >> 3][e & 7] = ml[0];
+            sh.l[e >> 3][e & 7] = ml[8 * NT];
+        }
+        __syncthreads();
+        {                                      // a warp a head: the maximum, then factors and sum
+            float mx = -INFINITY, sm = 0.f;
+            for (int j = lane; j < k; j += 32) mx = fmaxf(mx, sh.f[j][warp]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float base = mx == -INFINITY ? 0.f : mx;
+            for (int j = lane; j < k; j += 32) {
+                const float f = exp2_fast(sh.f[j][warp] - base);
+                sh.f[j][warp] = f;
+                sm += f * sh.l[j][warp];
+            }
+            sm = warp_sum(sm);
+            if (lane == 0) {
+                sh.sum[warp] = sm > 0.f ? 1.f / sm : 0.f;
+                sh.top[warp] = base;
+            }
+        }
+        __syncthreads();
+        float y0 = 0.f, y1 = 0.f;
+#pragma unroll 8
+        for (int j = warp; j < k; j += kJoinWarps) {
+            const float* src = part(b, j) + r0 * 32 + lane;
+            y0 += src[0] * sh.f[j][2 * (lane & 3)];
+            y1 += src[32] * sh.f[j][2 * (lane & 3) + 1];
+        }
+        sh.o[warp][0][lane] = y0;
+        sh.o[warp][1][lane] = y1;
+        __syncthreads();
+        if (warp < 2) {
+            float v = 0.f;
+#pragma unroll
+            for (int u = 0; u < kJoinWarps; ++u) v += sh.o[u][warp][lane];
+            int h, ch;
+            part_coord<D>(r0 + warp, lane, h, ch);
+            store_joined<T, D, NT>(p, n, head, h, ch, v * sh.sum[h & 7]);
+        }
+        if (r0 % (D / 4) == 0 && tid < 8) store_stats<NT>(p, n, head, nt * 8 + tid, sh.top[tid], sh.sum[tid]);
     }
-#pragma unroll
-    for (int r = 0; r < 8; ++r) s_o[warp][r][lane] = y[r];
-    __syncthreads();
-    const int g0 = head / p.GT * p.G, first = (head % p.GT) * 8 * NT;
-    static_assert(kJoinWarps == 8, "a warp a register and a head");
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) v += s_o[w][warp][lane];
-    int h, ch;
-    part_coord<D>(r0 + warp, lane, h, ch);
-    if (first + h < p.G) {
-        const float sm = s_sum[h & 7];
-        v = sm > 0.f ? v / sm : 0.f;
-        const int64_t at = ((int64_t)n * p.Hq + g0 + first + h) * D + ch;
-        if (p.z != nullptr) v *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
-        static_cast<T*>(p.o)[at] = from_f32<T>(v);
-    }
-    if (p.stats != nullptr && r0 % (D / 4) == 0 && tid < 8 && first + nt * 8 + tid < p.G)
-        p.stats[(int64_t)n * p.Hq + g0 + first + nt * 8 + tid] =
-            make_float2(s_top[tid], s_sum[tid] > 0.f ? 1.f / s_sum[tid] : 0.f);
 }
 
 // acc[n, h, j] += sum over the group's heads of exp2(score - max) / sum. Four slots a thread.
@@ -747,8 +838,7 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     paged_decode_kernel<T, D, NT><<<p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_after(paged_join_kernel<T, D, NT>, dim3(p.most_blocks, X::kRegs / 8), kJoinWarps * 32,
-                     stream, p);
+    e = launch_after(paged_join_kernel<T, D, NT>, dim3(sms * kJoinPerSm), kJoinWarps * 32, stream, p);
     if (e != cudaSuccess || a.acc == nullptr || a.max_len == 0) return e;
     const int64_t all = (int64_t)a.N * a.H * ((a.max_len + kWeightSlots - 1) / kWeightSlots);
     const unsigned grid = (unsigned)(all < sms * 16 ? all : sms * 16);
