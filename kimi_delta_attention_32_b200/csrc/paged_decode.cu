@@ -24,7 +24,7 @@
 //  - bf16: m16n8k16, P rounded to bf16 (each weight off by half a step, 2^-9 of it on average:
 //    below the rounding of the output itself); l sums the unrounded weights in fp32.
 //  - fp32: m16n8k8 TF32, each operand split in two (x = hi + lo, both TF32) and three products,
-//    which leaves 3 x 2^-22 of a product: fp32's own size.
+//    which leaves about 2^-20 of a product at most, and 2^-22 of it on average.
 //
 // Memory. Every warp owns a ring of S stages (16 K rows and 16 V rows each), filled by 16-byte
 // cp.async and waited for by its own lanes only. 16-byte piece c of row r lies at piece c ^ (r % 8):
@@ -77,10 +77,11 @@ __device__ __forceinline__ void mma_tf32(float* d, const uint32_t* a, uint32_t b
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo up to 2^-22 x, both TF32 values.
+// x = hi + lo up to 2^-21 x, both TF32 values (fp32 with 10 bits of fraction): hi is rounded to
+// the nearest, so |lo| <= 2^-11 x, and lo is cut. Four operations, fewer than two conversions take.
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(__uint_as_float(x) - __uint_as_float(hi)));
+    hi = (x + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) & 0xffffe000u;
 }
 // d += a b to fp32's accuracy: the two small cross products, then the large one.
 __device__ __forceinline__ void mma_f32(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -354,7 +355,9 @@ paged_decode_kernel(const Params p) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
         const int ar = lane & 15, ax = ar & 7, bx = lane & 7;
-#pragma unroll
+        // (fp32's 16 or 8 steps of three products and their splits are kept a loop: unrolled, the
+        // tile's code no longer fits the instruction cache)
+#pragma unroll (kBf16 ? X::kPieces / 4 : 1)
         for (int ks = 0; ks < X::kPieces / 2; ks += 2) {
             uint32_t a0[4], a1[4];
             ldsm4(kd + ar * X::kRowBytes + (((2 * ks + (lane >> 4)) ^ ax) << 4), a0);
@@ -430,7 +433,7 @@ paged_decode_kernel(const Params p) {
                 for (int nt = 0; nt < NT; ++nt) mma_bf16(out[nt][mt], a, pb[nt][0], pb[nt][1]);
             }
         } else {
-#pragma unroll
+#pragma unroll 1
             for (int half = 0; half < 2; ++half) {                 // 8 slots each
                 uint32_t pb[NT][2];
 #pragma unroll
@@ -438,8 +441,8 @@ paged_decode_kernel(const Params p) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {                  // slot lane % 4 + 4 e, head lane / 4
                         const int from = ((lane & 3) + 4 * e) * 4 + (lane >> 3);
-                        const float u = __shfl_sync(0xffffffffu, s[nt][2 * half], from);
-                        const float v = __shfl_sync(0xffffffffu, s[nt][2 * half + 1], from);
+                        const float u = __shfl_sync(0xffffffffu, half ? s[nt][2] : s[nt][0], from);
+                        const float v = __shfl_sync(0xffffffffu, half ? s[nt][3] : s[nt][1], from);
                         pb[nt][e] = __float_as_uint((lane >> 2) & 1 ? v : u);
                     }
 #pragma unroll
