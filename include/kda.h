@@ -418,7 +418,7 @@ kda_status kda_fused_recurrent_step(const void* q_raw, const void* k_raw, const 
  *  either sets the device error word, and kda_last_device_error then returns KDA_ERR_INDEX.
  *  Not checked: that no two slots share memory (a page twice in the tables of what one call
  *  writes), and finite inputs.
- *  Supported: d in {64, 128}, io F32 or BF16, any page_size.
+ *  Supported: d in {64, 128}, io F32 or BF16, any page_size, max_pages * page_size <= 2^30.
  */
 
 /*

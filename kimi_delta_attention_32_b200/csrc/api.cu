@@ -130,8 +130,8 @@ kda_status fill_cache(kda::PagedCache* c, const void* k_cache, const void* v_cac
     const int64_t per16 = io == KDA_IO_BF16 ? 8 : 4;          // elements of 16 bytes
     for (int64_t s : {page_stride, slot_stride, head_stride})
         if (s < d || s % per16 != 0) return KDA_ERR_INVALID_ARG;
-    // N Hkv counts blocks, and slots are int32
-    if ((int64_t)N * Hkv > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX)
+    // N Hkv counts blocks, and slots rounded up to whole tiles are int32
+    if ((int64_t)N * Hkv > INT32_MAX || (int64_t)max_pages * page_size > (1 << 30))
         return KDA_ERR_UNSUPPORTED;
     if (!head_dim_ok(d)) return KDA_ERR_UNSUPPORTED;
     c->k = const_cast<void*>(k_cache);

@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kMaxBlocks = 320;          // blocks of one launch: 2 an SM, for up to 160 SMs
 constexpr int kMergeFloats = 2048;       // shared floats for joining a block's warps
+constexpr float kSlack = 8.f;            // a score may exceed the running maximum by 2^8
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -47,6 +48,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
@@ -83,15 +87,17 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& l
     hi = (x + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) & 0xffffe000u;
 }
-// d += a b to fp32's accuracy: the two small cross products, then the large one.
-__device__ __forceinline__ void mma_f32(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+// d + dl + dh += a b to fp32's accuracy: the large product and the two small cross products, each
+// into its own accumulator (or the same one).
+__device__ __forceinline__ void mma_f32(float* d, float* dl, float* dh, const uint32_t* a, uint32_t b0,
+                                        uint32_t b1) {
     uint32_t ah[4], al[4], bh0, bh1, bl0, bl1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
     split_tf32(b0, bh0, bl0);
     split_tf32(b1, bh1, bl1);
-    mma_tf32(d, al, bh0, bh1);
-    mma_tf32(d, ah, bl0, bl1);
+    mma_tf32(dl, al, bh0, bh1);
+    mma_tf32(dh, ah, bl0, bl1);
     mma_tf32(d, ah, bh0, bh1);
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -131,6 +137,8 @@ struct Shape {
 
 struct Params {
     PagedCache c;
+    int64_t page_bytes, slot_bytes, head_bytes;
+    int step_pages, step_rows;       // a tile's slots, in whole pages and the rest
     const void *q, *z;
     const int32_t* seqlens;
     float scale_log2;
@@ -158,7 +166,8 @@ __device__ __forceinline__ void part_coord(int r, int lane, int& head, int& ch) 
     ch = mt * 16 + (lane >> 2) + 8 * (c >> 1);
 }
 
-template <typename T, int D, int NT>
+// kRuns: a page holds a multiple of 16 slots, so a warp's 16 lie in one page.
+template <typename T, int D, int NT, bool kRuns>
 __global__ void __launch_bounds__(Shape<T, D, NT>::W * 32, Shape<T, D, NT>::kPerSm)
 paged_decode_kernel(const Params p) {
     using X = Shape<T, D, NT>;
@@ -171,70 +180,70 @@ paged_decode_kernel(const Params p) {
     float* s_m = s_merge + kMergeFloats;                           // [W][8 NT]
     float* s_l = s_m + W * 8 * NT;
     uint32_t* s_live = reinterpret_cast<uint32_t*>(s_l + W * 8 * NT);   // [W][S] slots to attend to
-    __shared__ int64_t s_scan[W];
-    __shared__ int64_t s_first[2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int heads = p.H * p.GT;                                  // segments of a sequence
     const T* q = static_cast<const T*>(p.q);
 
-    // ---- the block's range of tiles
+    // ---- the block's range of tiles. Every warp finds it on its own: lane l sums the tiles of N / 32
+    // sequences, and the 32 sums tell whose sequences hold the first tile.
     auto len_of = [&](int n) { return checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err); };
     auto tiles_of = [&](int len) { return (len + kTile - 1) / kTile; };
-    auto block_scan = [&](int64_t x, int64_t* total) {             // exclusive
-        int64_t y = x;
+    auto warp_scan = [&](int x) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += u;
+            const int u = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += u;
         }
-        __syncthreads();
-        if (lane == 31) s_scan[warp] = y;
-        __syncthreads();
-        int64_t before = 0, sum = 0;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w < warp) before += s_scan[w];
-            sum += s_scan[w];
-        }
-        *total = sum;
-        return before + y - x;
+        return x;
     };
-    int64_t total = 0, mine = 0, excl;
-    for (int n = tid; n < p.N; n += kThreads) mine += tiles_of(len_of(n));
-    excl = block_scan(mine, &total);
-    const int64_t work = total * heads;
+    const int per = (p.N + 31) / 32, own0 = min(p.N, lane * per), own1 = min(p.N, own0 + per);
+    int mine = 0;
+#pragma unroll 4
+    for (int n = own0; n < own1; ++n) mine += tiles_of(len_of(n));
+    const int incl = warp_scan(mine);
+    const int64_t work = (int64_t)__shfl_sync(0xffffffffu, incl, 31) * heads;
     const int C = split_blocks(work, p.most_blocks), b = blockIdx.x;
     // sequences of length 0 have no tiles: their outputs are written here
-    for (int n = b; n < p.N; n += gridDim.x)
-        if (len_of(n) == 0)
-            for (int e = tid; e < p.Hq * D; e += kThreads)
-                static_cast<T*>(p.o)[(int64_t)n * p.Hq * D + e] = from_f32<T>(0.f);
-    if (tid == 0 && b < kMaxBlocks) p.meta[4 * b + 2] = -1;
-    if (b >= C) return;
+    auto write_empty = [&]() {
+        for (int n = b; n < p.N; n += gridDim.x)
+            if (len_of(n) == 0)
+                for (int e = tid; e < p.Hq * D; e += kThreads)
+                    static_cast<T*>(p.o)[(int64_t)n * p.Hq * D + e] = from_f32<T>(0.f);
+    };
+    if (tid == 0) p.meta[4 * b + 2] = -1;
+    if (b == 0 && warp == 0 && p.tiles_before != nullptr) {
+        int run = incl - mine;
+        for (int n = own0; n < own1; ++n) {
+            p.tiles_before[n] = run;
+            run += tiles_of(len_of(n));
+        }
+    }
+    if (b >= C) {
+        write_empty();
+        return;
+    }
     const int64_t t0 = split_begin(work, C, b);
     const int count = (int)(split_begin(work, C, b + 1) - t0);
+    const int target = (int)(t0 / heads);              // tiles of earlier sequences <= target
+    int first_n, first_before;
     {
-        const int64_t target = t0 / heads;                         // tiles of earlier sequences <= target
-        int64_t run = 0;
-        for (int base = 0; base < p.N; base += kThreads) {
-            const int n = base + tid;
-            int64_t x, sum, before;
-            if (p.N <= kThreads) {                                 // the scan above was this one
-                x = mine; sum = total; before = excl;
-            } else {
-                x = n < p.N ? tiles_of(len_of(n)) : 0;
-                before = block_scan(x, &sum);
+        const int owner = __ffs(__ballot_sync(0xffffffffu, mine > 0 && target < incl)) - 1;
+        first_n = owner * per;
+        first_before = __shfl_sync(0xffffffffu, incl - mine, owner);
+        const int end = min(p.N, first_n + per);
+        while (per > 1) {
+            const int x = first_n + lane < end ? tiles_of(len_of(first_n + lane)) : 0;
+            const int upto = first_before + warp_scan(x);
+            const unsigned here = __ballot_sync(0xffffffffu, x > 0 && target < upto);
+            if (here != 0) {
+                first_n += __ffs(here) - 1;
+                first_before = __shfl_sync(0xffffffffu, upto - x, __ffs(here) - 1);
+                break;
             }
-            if (n < p.N && b == 0 && p.tiles_before != nullptr) p.tiles_before[n] = (int)(run + before);
-            if (x > 0 && run + before <= target && target < run + before + x) {
-                s_first[0] = n;
-                s_first[1] = run + before;
-            }
-            run += sum;
-            if (run > target && !(b == 0 && p.tiles_before != nullptr)) break;
+            first_before = __shfl_sync(0xffffffffu, upto, 31);
+            first_n += 32;
         }
-        __syncthreads();
     }
 
     // ---- a position in the order of tiles: sequence, head (with its head tile), tile
@@ -251,58 +260,79 @@ paged_decode_kernel(const Params p) {
         u.tiles = tiles_of(u.len);
     };
     Cursor cur;
-    cur.n = (int)s_first[0];
+    cur.n = first_n;
     cur.len = len_of(cur.n);
     cur.tiles = tiles_of(cur.len);
     {
-        const int64_t in_seq = t0 - s_first[1] * heads;
+        const int64_t in_seq = t0 - (int64_t)first_before * heads;
         cur.head = (int)(in_seq / cur.tiles);
         cur.tile = (int)(in_seq % cur.tiles);
     }
 
-    // ---- loads. `ahead` is the tile whose page numbers are being fetched: lane l < 16 holds slot
-    // l of the warp's 16, and its page number is used only when the tile is loaded.
+    // ---- loads. `ahead` is the tile whose page number is being fetched, for use when the tile is
+    // loaded a step later: with kRuns of the warp's 16 slots, else lanes l and l + 16 of slot l's.
     Cursor ahead = cur;
-    int page = -1, row = 0, fetched = 0, loaded = 0, seg_loaded = -1;
-    bool live = false;
+    const int own = warp * 16 + (kRuns ? 0 : lane & 15);           // the lane's slot of a tile
+    const int own_page = own / p.c.page_size, own_row = own % p.c.page_size;
+    int at_page = (ahead.tile * kTile + own) / p.c.page_size, row = (ahead.tile * kTile + own) % p.c.page_size;
+    int page = -1, loaded = 0, seg_loaded = -1, st_loaded = 0;
     auto fetch = [&]() {
-        live = false;
-        if (fetched < count && lane < 16) {
-            const int slot = ahead.tile * kTile + warp * 16 + lane;
-            if (slot < ahead.len) {
-                live = true;
-                row = slot % p.c.page_size;
-                page = __ldg(p.c.block_table + (int64_t)ahead.n * p.c.max_pages + slot / p.c.page_size);
-            }
-        }
+        if (loaded < count && ahead.tile * kTile + own < ahead.len)
+            page = __ldg(p.c.block_table + (int64_t)ahead.n * p.c.max_pages + at_page);
     };
     uint8_t* ring = s_ring + (size_t)warp * S * X::kStage;
-    auto load = [&]() {          // tile `loaded` (= fetched): its rows, and its queries if it begins a segment
+    // row a of those that a warp instruction covers, 16-byte piece `piece`; rows r0 + a lie r0 rows
+    // on, with the piece's place exchanged by r0's low bits
+    constexpr int kRows = 32 / X::kPieces;
+    const int la = lane / X::kPieces, piece = lane % X::kPieces;
+    const uint32_t lane_dst = smem_u32(ring) + la * X::kRowBytes + ((piece ^ la) << 4);
+    const int64_t lane_src = (kRuns ? la * p.slot_bytes : 0) + piece * 16;
+    const uint8_t* kbase = static_cast<const uint8_t*>(p.c.k) + lane_src;
+    const uint8_t* vbase = static_cast<const uint8_t*>(p.c.v) + lane_src;
+    auto load = [&]() {          // tile `loaded`: its rows, and its queries if it begins a segment
         if (loaded < count) {
-            const int st = loaded % S, hkv = ahead.head / p.GT, gt = ahead.head % p.GT;
+            const int hkv = p.GT == 1 ? ahead.head : ahead.head / p.GT;
+            bool live = ahead.tile * kTile + own < ahead.len;
             if (live && (page < 0 || page >= p.c.num_pages)) {
                 atomicOr(p.c.err, kErrIndex);
                 live = false;
             }
-            const uint32_t mask = __ballot_sync(0xffffffffu, live);
-            if (lane == 0) s_live[warp * S + st] = mask;
-            const int64_t off = live ? (page * p.c.page_stride + row * p.c.slot_stride +
-                                        hkv * p.c.head_stride) * (int64_t)sizeof(T) : 0;
-            const uint32_t dst = smem_u32(ring + st * X::kStage);
-            constexpr int kRows = 32 / X::kPieces;       // rows a warp instruction covers
-            const int piece = lane % X::kPieces;
+            uint32_t mask;                             // of the 16 slots, those to attend to
+            if constexpr (kRuns) {
+                const int n = live ? min(16, ahead.len - ahead.tile * kTile - own) : 0;
+                mask = (1u << n) - 1;
+            } else {
+                mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
+            }
+            if (lane == 0) s_live[warp * S + st_loaded] = mask;
+            const int64_t off = live ? page * p.page_bytes + row * p.slot_bytes + hkv * p.head_bytes : 0;
+            const uint32_t dst = lane_dst + st_loaded * X::kStage;
+            if (kRuns && mask == 0xffffu) {
+                const uint8_t *k = kbase + off, *v = vbase + off;
 #pragma unroll
-            for (int r0 = 0; r0 < 16; r0 += kRows) {
-                const int r = r0 + lane / X::kPieces;
-                const int64_t from = __shfl_sync(0xffffffffu, off, r) + piece * 16;
-                const bool ok = mask >> r & 1;
-                const uint32_t to = dst + r * X::kRowBytes + ((piece ^ (r & 7)) << 4);
-                cp_async16(to, static_cast<const uint8_t*>(p.c.k) + (ok ? from : 0), ok);
-                cp_async16(to + 16 * X::kRowBytes, static_cast<const uint8_t*>(p.c.v) + (ok ? from : 0), ok);
+                for (int r0 = 0; r0 < 16; r0 += kRows) {
+                    const uint32_t to = (dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4);
+                    cp_async16(to, k);
+                    cp_async16(to + 16 * X::kRowBytes, v);
+                    k += kRows * p.slot_bytes;
+                    v += kRows * p.slot_bytes;
+                }
+            } else {
+#pragma unroll
+                for (int r0 = 0; r0 < 16; r0 += kRows) {
+                    const uint32_t to = (dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4);
+                    const bool ok = mask >> (r0 + la) & 1;
+                    int64_t from = off;
+                    if constexpr (kRuns) from = ok ? off + r0 * p.slot_bytes : 0;
+                    else from = __shfl_sync(0xffffffffu, off, r0 + la);
+                    cp_async16(to, kbase + from, ok);
+                    cp_async16(to + 16 * X::kRowBytes, vbase + from, ok);
+                }
             }
             if (loaded == 0 || ahead.tile == 0) {
-                ++seg_loaded;
-                const uint32_t qd = smem_u32(s_q + (size_t)(seg_loaded % S) * X::kQ);
+                if (++seg_loaded == S) seg_loaded = 0;
+                const int gt = ahead.head - hkv * p.GT;
+                const uint32_t qd = smem_u32(s_q + (size_t)seg_loaded * X::kQ);
                 for (int e = tid; e < 8 * NT * X::kPieces; e += kThreads) {
                     const int g = e / X::kPieces, pc = e % X::kPieces, hg = gt * 8 * NT + g;
                     const bool ok = hg < p.G;
@@ -311,10 +341,21 @@ paged_decode_kernel(const Params p) {
                                reinterpret_cast<const uint8_t*>(src) + pc * 16, ok);
                 }
             }
-            ++loaded;
-            ++fetched;
-            if (fetched < count) next(ahead);
-            fetch();
+            if (++st_loaded == S) st_loaded = 0;
+            if (++loaded < count) {
+                next(ahead);
+                at_page += p.step_pages;
+                row += p.step_rows;
+                if (row >= p.c.page_size) {
+                    row -= p.c.page_size;
+                    ++at_page;
+                }
+                if (ahead.tile == 0) {
+                    at_page = own_page;
+                    row = own_row;
+                }
+                fetch();
+            }
         }
         cp_commit();
     };
@@ -323,11 +364,12 @@ paged_decode_kernel(const Params p) {
     for (int i = 0; i < S - 1; ++i) load();
 
     // ---- the tiles
-    float out[NT][D / 16][4], m[NT][2], l[NT][2];
+    float out[NT][D / 16][4], m[NT][2], base[NT][2], l[NT][2];     // base: m, or 0 while m is -inf
     auto reset = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
+            base[nt][0] = base[nt][1] = 0.f;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt)
@@ -336,24 +378,30 @@ paged_decode_kernel(const Params p) {
         }
     };
     reset();
-    int seg = 0;
+    int st = -1, st_q = 0;
     bool from_start = cur.tile == 0;               // the segment begins in this block
+#pragma unroll 1
     for (int i = 0; i < count; ++i) {
         cp_wait<S - 2>();
         __syncwarp();
         load();                                    // into the stage read in the step before
-        const int st = i % S;
+        if (++st == S) st = 0;
         if (i == 0 || cur.tile == 0) __syncthreads();              // the segment's queries are there
-        const uint32_t kd = smem_u32(ring + st * X::kStage), vd = kd + 16 * X::kRowBytes;
-        const uint32_t qd = smem_u32(s_q + (size_t)(seg % S) * X::kQ);
+        const uint32_t kd = smem_u32(ring) + st * X::kStage, vd = kd + 16 * X::kRowBytes;
+        const uint32_t qd = smem_u32(s_q) + st_q * X::kQ;
         const uint32_t mask = s_live[warp * S + st];
 
-        // S^T = K Q^T: rows slots, columns heads. Two accumulators halve the chain.
-        float s[NT][4], s2[NT][4];
+        // S^T = K Q^T: rows slots, columns heads. Several accumulators shorten the chain.
+        constexpr int kAccs = kBf16 ? 2 : 3;
+        float s[NT][4], sx[kAccs - 1][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
+            for (int c = 0; c < 4; ++c) {
+                s[nt][c] = 0.f;
+#pragma unroll
+                for (int u = 0; u < kAccs - 1; ++u) sx[u][nt][c] = 0.f;
+            }
         const int ar = lane & 15, ax = ar & 7, bx = lane & 7;
         // (fp32's 16 or 8 steps of three products and their splits are kept a loop: unrolled, the
         // tile's code no longer fits the instruction cache)
@@ -368,52 +416,63 @@ paged_decode_kernel(const Params p) {
                 ldsm4(qd + (nt * 8 + bx) * X::kRowBytes + (((2 * ks + (lane >> 3)) ^ bx) << 4), bq);
                 if constexpr (kBf16) {
                     mma_bf16(s[nt], a0, bq[0], bq[1]);
-                    mma_bf16(s2[nt], a1, bq[2], bq[3]);
+                    mma_bf16(sx[0][nt], a1, bq[2], bq[3]);
                 } else {
-                    mma_f32(s[nt], a0, bq[0], bq[1]);
-                    mma_f32(s2[nt], a1, bq[2], bq[3]);
+                    mma_f32(s[nt], sx[0][nt], sx[kAccs - 2][nt], a0, bq[0], bq[1]);
+                    mma_f32(s[nt], sx[0][nt], sx[kAccs - 2][nt], a1, bq[2], bq[3]);
                 }
             }
         }
         const bool ok0 = mask >> (lane >> 2) & 1, ok1 = mask >> ((lane >> 2) + 8) & 1;
-        float corr[NT][2];
-        bool moved = false;
+        bool above = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float x[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                x[c] = (c < 2 ? ok0 : ok1) ? (s[nt][c] + s2[nt][c]) * p.scale_log2 : -INFINITY;
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int u = kAccs - 2; u > 0; --u) sx[u - 1][nt][c] += sx[u][nt][c];
+                s[nt][c] = (c < 2 ? ok0 : ok1) ? (s[nt][c] + sx[0][nt][c]) * p.scale_log2 : -INFINITY;
+                above |= s[nt][c] > m[nt][c & 1] + kSlack;
+            }
             if (p.scores != nullptr) {
                 float* w = p.scores + (t0 + i) * p.GS * kTile + warp * 16 + (lane >> 2);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int g = nt * 8 + 2 * (lane & 3) + (c & 1);
-                    if (g < p.GS) w[g * kTile + 8 * (c >> 1)] = x[c];
+                    if (g < p.GS) w[g * kTile + 8 * (c >> 1)] = s[nt][c];
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(x[e], x[e + 2]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                const float mn = fmaxf(m[nt][e], mx), base = mn == -INFINITY ? 0.f : mn;
-                corr[nt][e] = exp2_fast(m[nt][e] - base);
-                moved |= mn != m[nt][e];
-                m[nt][e] = mn;
-                s[nt][e] = exp2_fast(x[e] - base);
-                s[nt][e + 2] = exp2_fast(x[e + 2] - base);
-                l[nt][e] = l[nt][e] * corr[nt][e] + s[nt][e] + s[nt][e + 2];
-            }
         }
-        if (__any_sync(0xffffffffu, moved)) {
+        // The running maximum moves only when a score passes it by kSlack: until then the weights
+        // stay below 2^kSlack, as exact as below 1, and no lane has to ask the others.
+        if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float corr[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const float mn = fmaxf(m[nt][e], mx);
+                    base[nt][e] = mn == -INFINITY ? 0.f : mn;
+                    corr[e] = exp2_fast(m[nt][e] - base[nt][e]);
+                    m[nt][e] = mn;
+                    l[nt][e] *= corr[e];
+                }
 #pragma unroll
                 for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) out[nt][mt][c] *= corr[nt][c & 1];
+                    for (int c = 0; c < 4; ++c) out[nt][mt][c] *= corr[c & 1];
+            }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                s[nt][c] = exp2_fast(s[nt][c] - base[nt][c & 1]);
+                l[nt][c & 1] += s[nt][c];
+            }
         // O^T += V^T P^T: rows channels, columns heads
         if constexpr (kBf16) {
             uint32_t pb[NT][2];
@@ -457,7 +516,7 @@ paged_decode_kernel(const Params p) {
                             (((ch >> 2) ^ (r & 7)) << 4) + (ch & 3) * 4);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f32(out[nt][mt], a, pb[nt][0], pb[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_f32(out[nt][mt], out[nt][mt], out[nt][mt], a, pb[nt][0], pb[nt][1]);
                 }
             }
         }
@@ -550,13 +609,14 @@ paged_decode_kernel(const Params p) {
                 p.meta[4 * b + 2] = split_block_of(work, C, last);
             }
             reset();
-            ++seg;
+            if (++st_q == S) st_q = 0;
             from_start = true;
         }
         if (i + 1 < count) next(cur);
     }
     cp_wait<0>();
     grid_release();
+    write_empty();
 }
 
 // Joins the parts of every segment that spans blocks, by two kinds of work items:
@@ -819,6 +879,11 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     Params p;
     p.c = a.c;
+    p.page_bytes = a.c.page_stride * (int64_t)sizeof(T);
+    p.slot_bytes = a.c.slot_stride * (int64_t)sizeof(T);
+    p.head_bytes = a.c.head_stride * (int64_t)sizeof(T);
+    p.step_pages = X::kTile / a.c.page_size;
+    p.step_rows = X::kTile % a.c.page_size;
     p.q = a.q; p.z = a.z;
     p.seqlens = a.seqlens;
     p.scale_log2 = a.scale * 1.4426950408889634f;
@@ -836,10 +901,14 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     p.GS = p.G < 8 * NT ? p.G : 8 * NT;
     p.acc = a.acc;
     p.slots = a.slots;
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(paged_decode_kernel<T, D, NT>, X::kSmem, allowed);
+    // pages of a multiple of 16 slots, the common ones, need one page number a warp and no exchange
+    // of row addresses between lanes
+    static std::atomic<uint64_t> allowed[2];
+    const bool runs = a.c.page_size % 16 == 0;
+    auto kernel = runs ? paged_decode_kernel<T, D, NT, true> : paged_decode_kernel<T, D, NT, false>;
+    cudaError_t e = allow_smem(kernel, X::kSmem, allowed[runs]);
     if (e != cudaSuccess) return e;
-    paged_decode_kernel<T, D, NT><<<p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
+    kernel<<<p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_after(paged_join_kernel<T, D, NT>, dim3(sms * kJoinPerSm), kJoinWarps * 32, stream, p);
     if (e != cudaSuccess || a.acc == nullptr || a.max_len == 0) return e;
@@ -863,7 +932,8 @@ cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
 bool paged_decode_workspace(int64_t N, int64_t Hq, int64_t H, int d, int64_t max_len, bool with_acc,
                             size_t* bytes) {
     const double scores = (double)N * H * (Hq / H + 32) * (max_len + 128) * 4;
-    if (N * Hq > INT32_MAX || scores > 4e18) return false;
+    // tiles of all sequences count in 31 bits
+    if (N * Hq > INT32_MAX || N * (max_len / 64 + 1) > INT32_MAX || scores > 4e18) return false;
     size_t most = 0;                     // whichever io: bf16 and fp32 differ in their head tiles
     for (bool bf16 : {false, true}) {
         const int NT = head_tiles(Hq / H, bf16);
