@@ -20,6 +20,8 @@
 // read and written once).
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace kda {
@@ -30,9 +32,10 @@ namespace cg = cooperative_groups;
 constexpr int kMaxKeys = 49152;           // keys of one block in shared memory: 192 KB
 constexpr int kBins = 2048;               // histogram of one pass (three of them: 24 KB)
 constexpr int kMaxCluster = 8;
+constexpr int kRun = 128;                 // slots that a warp walks at a time
 
 // Rank key of an entry: order-preserving bits of the fp32 weight (NaN lowest, -0 equal to 0).
-__device__ __forceinline__ uint32_t rank_key(float acc, int64_t pos, int n_first, int64_t recent_from) {
+__device__ __forceinline__ uint32_t rank_key(float acc, int pos, int n_first, int recent_from) {
     if (pos < n_first || pos >= recent_from) return 0xffffffffu;
     if (acc != acc) return 0u;
     const uint32_t b = __float_as_uint(acc + 0.f);
@@ -47,36 +50,14 @@ struct SelectArgs {
     int keys;                 // keys a block holds in shared memory, 0: none
 };
 
-// Exclusive prefix sum of x over the block; *total receives the sum.
-template <int kThreads>
-__device__ __forceinline__ int block_scan(int x, int* buf, int* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto warp_scan = [&](int y) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        return y;
-    };
-    const int y = warp_scan(x);
-    __syncthreads();
-    if (lane == 31) buf[warp] = y;
-    __syncthreads();
-    const int sums = warp_scan(lane < kThreads / 32 ? buf[lane] : 0);      // every warp on its own
-    *total = __shfl_sync(0xffffffffu, sums, 31);
-    const int before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
-    return (warp > 0 ? before : 0) + y - x;
-}
-
 // kMany: the cluster has more than one block.
 template <int kThreads, bool kMany>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs s) {
-    extern __shared__ uint32_t s_keys[];
-    __shared__ int s_hist[3][kBins];
-    __shared__ int s_buf[kThreads / 32], s_pick[2];
-    __shared__ int s_share[4];                           // this block's counts, read by the cluster
+    extern __shared__ __align__(16) uint32_t s_keys[];
     constexpr int kWarps = kThreads / 32, kAhead = 8;    // kAhead: entries a thread loads at once
+    __shared__ int s_hist[3][kBins], s_coarse[3][kBins / 32];
+    __shared__ int s_pick[2];
+    __shared__ int s_warp[kWarps][4], s_share[4];        // counts of the warps, and of the block
     const EvictArgs& a = s.e;
     int CS = 1, rank = 0;
     if constexpr (kMany) {
@@ -90,7 +71,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
     const int64_t nh = blockIdx.x / CS, n = nh / a.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int len = checked_len(a.seqlens[n], a.max_len, a.c.err);
-    const int64_t recent_from = (int64_t)a.positions[n] - a.n_recent, at = nh * a.slots;
+    const int64_t at = nh * a.slots;
+    const int recent_from = (int)max((int64_t)INT32_MIN, (int64_t)a.positions[n] - a.n_recent);
     const bool copy_acc = a.acc_out != a.acc, copy_pos = a.pos_out != a.pos;
 
     if (len <= a.keep || a.keep == 0) {                  // nothing moves (the whole cluster agrees)
@@ -102,13 +84,22 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
         if (rank == 0 && tid == 0) s.counts[nh] = 0;
         return;
     }
-    // the block's slots [lo, hi), a warp's a contiguous run of whole 32s of them
-    const int per_warp = ((len + CS * kThreads - 1) / (CS * kThreads)) * 32;
+    // the block's slots [lo, hi), a warp's a contiguous run of whole kRun of them
+    const int per_warp = (len + CS * kWarps * kRun - 1) / (CS * kWarps * kRun) * kRun;
     const int lo = min(len, rank * kWarps * per_warp);
     const int hi = min(len, lo + kWarps * per_warp);
     const bool held = hi - lo <= s.keys;
-    auto fresh = [&](int j) { return rank_key(a.acc[at + j], a.pos[at + j], a.n_first, recent_from); };
-    auto key = [&](int j) { return held ? s_keys[j - lo] : fresh(j); };
+    auto key = [&](int j) { return rank_key(a.acc[at + j], a.pos[at + j], a.n_first, recent_from); };
+    // the keys of four slots from j on, j a multiple of 4; those at `end` and behind say nothing
+    auto keys4 = [&](int j, int end, uint32_t (&k)[4]) {
+        if (held) {
+            const uint4 v = *reinterpret_cast<const uint4*>(s_keys + (j < end ? j - lo : 0));
+            k[0] = v.x; k[1] = v.y; k[2] = v.z; k[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = j + i < end ? key(j + i) : 0;
+        }
+    };
 
     for (int i = tid; i < 3 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0;
     __syncthreads();
@@ -158,34 +149,64 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
                 }
             }
         } else {
-            for (int base = lo; base < hi; base += kThreads) {
-                const int j = base + tid;
-                count(j < hi ? key(j) : 0, j < hi);
+            for (int base = lo; base < hi; base += kThreads * 4) {
+                const int j = base + tid * 4;
+                uint32_t k[4];
+                keys4(j, hi, k);
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) any |= j + i < hi && (k[i] & above) == (T & above);
+                if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) count(k[i], j + i < hi);
             }
+        }
+        __syncthreads();
+        // sums of 32 bins; one warp then finds the 32 and the bin, from all blocks' histograms
+        for (int g = warp; g < kBins / 32; g += kWarps) {
+            const int sum = __reduce_add_sync(0xffffffffu, s_hist[pass][g * 32 + lane]);
+            if (lane == 0) s_coarse[pass][g] = sum;
         }
         sync_all();
-        constexpr int kPer = kBins / kThreads;           // bins a thread sums, from the top down
-        int c[kPer], mine = 0, total;
+        if (warp == 0) {
+            // the value of bin i, summed over the cluster
+            auto sum_over = [&](int* bins, int i) {
+                if constexpr (!kMany) return bins[i];
+                int v = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) c[i] = 0;
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < CS) v += cg::this_cluster().map_shared_rank(bins, r)[i];
+                return v;
+            };
+            // of 32 counts, lane l's the l-th from the top: the lane at which `left` is reached
+            auto reach = [&](int c, int& over) {
+                int upto = c;
 #pragma unroll
-        for (int r = 0; r < (kMany ? kMaxCluster : 1); ++r) {
-            if (r >= CS) break;
-            const int* hist = s_hist[pass];
-            if constexpr (kMany) hist = cg::this_cluster().map_shared_rank(&s_hist[pass][0], r);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) c[i] += hist[kBins - 1 - (tid * kPer + i)];
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) mine += c[i];
-        int over = block_scan<kThreads>(mine, s_buf, &total);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (over < left && left <= over + c[i]) {
-                s_pick[0] = kBins - 1 - (tid * kPer + i);
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += u;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, upto >= left);
+                const int at_lane = __ffs(hit) - 1;      // -1: not among these
+                over = __shfl_sync(0xffffffffu, at_lane < 0 ? upto : upto - c, at_lane < 0 ? 31 : at_lane);
+                return at_lane;
+            };
+            const int upper = sum_over(s_coarse[pass], kBins / 32 - 1 - lane);
+            const int lower = sum_over(s_coarse[pass], kBins / 64 - 1 - lane);
+            int over, group = reach(upper, over);
+            if (group >= 0) {
+                group = kBins / 32 - 1 - group;
+                left -= over;
+            } else {
+                left -= over;
+                group = kBins / 64 - 1 - reach(lower, over);
+                left -= over;
+            }
+            const int bin = 31 - reach(sum_over(s_hist[pass] + group * 32, 31 - lane), over);
+            if (lane == 0) {
+                s_pick[0] = group * 32 + bin;
                 s_pick[1] = left - over;
             }
-            over += c[i];
         }
         __syncthreads();
         T |= (uint32_t)s_pick[0] << shift;
@@ -195,57 +216,91 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
     // ---- Of the entries with key T the `left` lowest slots stay, so what is kept before a slot
     // follows from four counts before it: keys above T and keys equal to T, in front (slots < keep)
     // and behind. Front slots come first, so the kept ties in front are min(left, ties in front).
+    // A lane takes four slots at a time.
     const int w0 = min(hi, lo + warp * per_warp), w1 = min(hi, w0 + per_warp);
     int cnt[4] = {0, 0, 0, 0};                           // above in front, behind; ties in front, behind
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t k = j < w1 ? key(j) : 0;
-        const unsigned up = __ballot_sync(0xffffffffu, j < w1 && k > T);
-        const unsigned tie = __ballot_sync(0xffffffffu, j < w1 && k == T);
-        const unsigned in_front = __ballot_sync(0xffffffffu, j < a.keep);
-        cnt[0] += __popc(up & in_front);
-        cnt[1] += __popc(up & ~in_front);
-        cnt[2] += __popc(tie & in_front);
-        cnt[3] += __popc(tie & ~in_front);
+    for (int j = w0 + 4 * lane; j < w1; j += kRun) {
+        uint32_t k[4];
+        keys4(j, w1, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = j + i < w1, front = j + i < a.keep;
+            cnt[0] += in && front && k[i] > T;
+            cnt[1] += in && !front && k[i] > T;
+            cnt[2] += in && front && k[i] == T;
+            cnt[3] += in && !front && k[i] == T;
+        }
     }
-    int all[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        cnt[i] = block_scan<kThreads>(lane == 0 ? cnt[i] : 0, s_buf, &all[i]);
-        cnt[i] = __shfl_sync(0xffffffffu, cnt[i], 0);
+        cnt[i] = __reduce_add_sync(0xffffffffu, cnt[i]);
+        if (lane == 0) s_warp[warp][i] = cnt[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                        // before this warp, and of the whole block
+        const int v = lane < kWarps ? s_warp[lane][i] : 0;
+        cnt[i] = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+        if constexpr (kMany) {
+            const int all = __reduce_add_sync(0xffffffffu, v);
+            if (tid == 0) s_share[i] = all;
+        }
     }
     if constexpr (kMany) {
-        if (tid < 4) s_share[tid] = tid == 0 ? all[0] : tid == 1 ? all[1] : tid == 2 ? all[2] : all[3];
         cg::this_cluster().sync();
-        for (int r = 0; r < rank; ++r) {
-            const int* share = cg::this_cluster().map_shared_rank(&s_share[0], r);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) cnt[i] += share[i];
+        for (int i = 0; i < 4; ++i) {
+            const int v = lane < rank ? cg::this_cluster().map_shared_rank(&s_share[0], lane)[i] : 0;
+            cnt[i] += __reduce_add_sync(0xffffffffu, v);
         }
     }
     int* hole = s.lists + nh * 2 * s.most;
     int* tail = hole + s.most;
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t k = j < w1 ? key(j) : 0;
-        const unsigned up = __ballot_sync(0xffffffffu, j < w1 && k > T);
-        const unsigned tie = __ballot_sync(0xffffffffu, j < w1 && k == T);
-        const unsigned in_front = __ballot_sync(0xffffffffu, j < a.keep);
-        const unsigned before = (1u << lane) - 1;
-        // counts before slot j
-        const int up_f = cnt[0] + __popc(up & in_front & before), up_b = cnt[1] + __popc(up & ~in_front & before);
-        const int tie_f = cnt[2] + __popc(tie & in_front & before), tie_b = cnt[3] + __popc(tie & ~in_front & before);
-        const int stay_f = min(left, tie_f), stay_b = min(left, tie_f + tie_b) - stay_f;
-        const bool kept = (up >> lane & 1) || ((tie >> lane & 1) && tie_f + tie_b < left);
-        if (j < w1) {
-            if (j < a.keep && !kept) hole[j - (up_f + stay_f)] = j;
-            if (j >= a.keep && kept) tail[up_b + stay_b] = j;
+    // the slots [from, to) of one side: a front slot that goes is a hole, a slot behind that stays
+    // fills one
+    auto list = [&](auto is_front, int from, int to) {
+        constexpr bool kFront = decltype(is_front)::value;
+        int up = kFront ? cnt[0] : cnt[1], ties = cnt[2] + (kFront ? 0 : cnt[3]);
+        const int stay_f = min(left, cnt[2]);            // (for the slots behind: all front ties kept)
+        if (from >= to) return;                          // (a block behind the end has no keys to read)
+        for (int j0 = from & ~(kRun - 1); j0 < to; j0 += kRun) {
+            const int j = j0 + 4 * lane;
+            uint32_t k[4], one[4], mine = 0;             // counts: above in the low half, ties in the high
+            keys4(j, w1, k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                one[i] = j + i < from || j + i >= to || k[i] < T ? 0u : k[i] > T ? 1u : 0x10000u;
+                mine += one[i];
+            }
+            uint32_t upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += u;
+            }
+            const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+            upto -= mine;                                // before this lane's first slot
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tied = ties + (int)(upto >> 16), above = up + (int)(upto & 0xffffu);
+                const bool kept = one[i] == 1u || (one[i] != 0 && tied < left);
+                const int before = above + min(left, tied) - (kFront ? 0 : stay_f);   // kept before j + i
+                if constexpr (kFront) {
+                    if (!kept && j + i >= from && j + i < to) hole[j + i - before] = j + i;
+                } else {
+                    if (kept) tail[before] = j + i;
+                }
+                upto += one[i];
+            }
+            up += (int)(all & 0xffffu);
+            ties += (int)(all >> 16);
         }
-        cnt[0] += __popc(up & in_front);
-        cnt[1] += __popc(up & ~in_front);
-        cnt[2] += __popc(tie & in_front);
-        cnt[3] += __popc(tie & ~in_front);
-    }
+        cnt[kFront ? 0 : 1] = up;
+        if constexpr (kFront) cnt[2] = ties;
+        else cnt[3] = ties - cnt[2];
+    };
+    list(std::true_type{}, w0, min(w1, a.keep));
+    list(std::false_type{}, max(w0, a.keep), w1);
     // after the last warp's slots: all that is kept behind keep
     if (rank == CS - 1 && tid == kThreads - 1)
         s.counts[nh] = cnt[1] + min(left, cnt[2] + cnt[3]) - min(left, cnt[2]);
@@ -257,6 +312,7 @@ template <int kPieces>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const SelectArgs s, int chunks, int esz) {
     __shared__ int64_t s_to[kMoveRows], s_from[kMoveRows];
     const EvictArgs& a = s.e;
+    grid_wait();
     const int64_t nh = blockIdx.x / chunks, n = nh / a.H, at = nh * a.slots;
     const int h = (int)(nh % a.H), first = (int)(blockIdx.x % chunks) * kMoveRows, tid = threadIdx.x;
     if (h == 0 && first == 0 && tid == 0)      // after every head's select has read seqlens
@@ -356,12 +412,14 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     s.most = (int)most_moves(a.max_len, a.keep);
     s.counts = static_cast<int*>(a.workspace);
     s.lists = s.counts + (int64_t)a.N * a.H;
-    // a block for up to 8192 slots, 8 at most; below 2048 slots fewer threads meet at the barriers
+    // a block for up to 8192 slots, 8 at most: of clusters of 16 only 7 fit the GPU at once (of 8,
+    // 15), so that the 8 heads of one long sequence took two waves of them, 60 us for 45. Below 2048
+    // slots fewer threads meet at the barriers.
     int cluster = 1;
     while (cluster < kMaxCluster && (int64_t)cluster * 8192 < a.max_len) cluster *= 2;
     const bool small = a.max_len <= 2048;
-    const int round = cluster * (small ? 256 : 1024);    // a block's slots come in whole rounds
-    const int64_t need = ((int64_t)a.max_len + round - 1) / round * (small ? 256 : 1024);
+    const int block = (small ? 256 : 1024) / 32 * kRun;  // a block's slots come in whole runs of its warps
+    const int64_t need = ((int64_t)a.max_len + cluster * block - 1) / (cluster * block) * block;
     s.keys = need <= kMaxKeys ? (int)need : 0;
     const size_t smem = (size_t)s.keys * 4;
     cudaError_t e = small         ? launch_select<256, false>(s, 1, smem, stream)
@@ -372,12 +430,11 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     const int chunks = s.most > 0 ? (s.most + kMoveRows - 1) / kMoveRows : 1;
     const unsigned grid = (unsigned)((int64_t)a.N * a.H * chunks);
     switch (a.d * esz / 16) {
-        case 8: evict_move_kernel<8><<<grid, kMoveThreads, 0, stream>>>(s, chunks, esz); break;
-        case 16: evict_move_kernel<16><<<grid, kMoveThreads, 0, stream>>>(s, chunks, esz); break;
-        case 32: evict_move_kernel<32><<<grid, kMoveThreads, 0, stream>>>(s, chunks, esz); break;
-        default: return cudaErrorInvalidValue;
+        case 8: return launch_after(evict_move_kernel<8>, grid, kMoveThreads, stream, s, chunks, esz);
+        case 16: return launch_after(evict_move_kernel<16>, grid, kMoveThreads, stream, s, chunks, esz);
+        case 32: return launch_after(evict_move_kernel<32>, grid, kMoveThreads, stream, s, chunks, esz);
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace kda

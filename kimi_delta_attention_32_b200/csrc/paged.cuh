@@ -31,18 +31,42 @@ __device__ __forceinline__ int64_t slot_offset(const PagedCache& c, int64_t n, i
     return page * c.page_stride + (slot % c.page_size) * c.slot_stride;
 }
 
-// Raises a kernel's limit of dynamic shared memory, once per device: `done` (one per kernel) has a
-// bit for each of the first 64 devices.
+// Programmatic dependent launch: a kernel launched with launch_after may start while the one before
+// it on the stream ends; it waits here until that one has finished and its writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launches a kernel that begins with grid_wait().
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// Sets an attribute of a kernel, once per device: `done` (one per kernel and attribute) has a bit
+// for each of the first 64 devices.
 template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+cudaError_t set_once(K kernel, cudaFuncAttribute attr, int value, std::atomic<uint64_t>& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    e = cudaFuncSetAttribute(kernel, attr, value);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
+}
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    return set_once(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes, done);
 }
 
 }  // namespace kda

@@ -421,7 +421,8 @@ def test_evict_positions():
 
 
 @pytest.mark.parametrize("length,keep", [(5000, 4096), (4097, 4096), (70000, 30000), (70000, 69990),
-                                         (70000, 3), (1025, 1000)])
+                                         (70000, 3), (1025, 1000), (2048, 700), (2049, 700),
+                                         (8193, 4000), (17000, 9000), (262145, 100000)])
 def test_evict_long(length, keep):
     c = Paged("bf16", [length, length // 2, 10], 1, 64, 64, seed=length)
     evict_case(c, keep, 2 if keep > 3 else 0, keep // 4)
