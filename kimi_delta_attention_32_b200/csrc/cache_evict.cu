@@ -413,18 +413,18 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     s.counts = static_cast<int*>(a.workspace);
     s.lists = s.counts + (int64_t)a.N * a.H;
     // a block for up to 8192 slots, 8 at most: of clusters of 16 only 7 fit the GPU at once (of 8,
-    // 15), so that the 8 heads of one long sequence took two waves of them, 60 us for 45. Below 2048
-    // slots fewer threads meet at the barriers.
+    // 15), so that the 8 heads of one long sequence took two waves of them, 60 us for 45. Shorter
+    // caches take fewer threads: fewer meet at the barriers, and more blocks share an SM.
     int cluster = 1;
     while (cluster < kMaxCluster && (int64_t)cluster * 8192 < a.max_len) cluster *= 2;
-    const bool small = a.max_len <= 2048;
-    const int block = (small ? 256 : 1024) / 32 * kRun;  // a block's slots come in whole runs of its warps
+    const int threads = a.max_len <= 2048 ? 256 : cluster == 1 ? 512 : 1024;
+    const int block = threads / 32 * kRun;               // a block's slots come in whole runs of its warps
     const int64_t need = ((int64_t)a.max_len + cluster * block - 1) / (cluster * block) * block;
     s.keys = need <= kMaxKeys ? (int)need : 0;
     const size_t smem = (size_t)s.keys * 4;
-    cudaError_t e = small         ? launch_select<256, false>(s, 1, smem, stream)
-                    : cluster > 1 ? launch_select<1024, true>(s, cluster, smem, stream)
-                                  : launch_select<1024, false>(s, 1, smem, stream);
+    const cudaError_t e = threads == 256   ? launch_select<256, false>(s, 1, smem, stream)
+                          : threads == 512 ? launch_select<512, false>(s, 1, smem, stream)
+                                           : launch_select<1024, true>(s, cluster, smem, stream);
     if (e != cudaSuccess) return e;
     const int esz = a.io == Io::BF16 ? 2 : 4;
     const int chunks = s.most > 0 ? (s.most + kMoveRows - 1) / kMoveRows : 1;
