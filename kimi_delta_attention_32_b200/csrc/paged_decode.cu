@@ -840,17 +840,6 @@ Layout layout(int64_t N, int64_t Hq, int64_t H, int64_t max_len, bool with_acc, 
     return l;
 }
 
-// SMs of the current device (0 if the query fails); cached per device.
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 template <typename T, int D, int NT>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     using X = Shape<T, D, NT>;
