@@ -144,8 +144,8 @@ struct Params {
     int most_blocks;
     int* meta;                       // [blocks][4]: n, head * GT + gt, last block of a segment to join
     float* parts;                    // [2 blocks][kPart]: a block's first and last segments' parts
-    // for acc: scores (log2 units) [tile][GS][kTile], {max, 1 / sum} [N, Hq], and tiles of the
-    // sequences before n [N + 1]
+    // for acc: scores (log2 units) [tile][GS][kTile]; {max, 1 / sum} [N, Hq] of the segments inside
+    // one block; and the tiles of the sequences before n, of one head [N + 1]
     float* scores;
     float2* stats;
     int* tiles_before;
@@ -214,6 +214,7 @@ paged_decode_kernel(const Params p) {
             p.tiles_before[n] = run;
             run += tiles_of(len_of(n));
         }
+        if (lane == 31) p.tiles_before[p.N] = incl;
     }
     if (b >= C) {
         write_empty();
@@ -615,18 +616,97 @@ paged_decode_kernel(const Params p) {
     write_empty();
 }
 
+constexpr int kJoinWarps = 8, kJoinPerSm = 4, kFew = 8;
+
+// acc[n, h, j] += sum over the group's heads of exp2(score - max) / sum: 1024 slots of one head a
+// block, four a thread. The maximum and sum of a segment that spans blocks come from its parts, so
+// this does not wait for the join of the outputs and shares its launch.
+constexpr int kWeightSlots = 4 * kJoinWarps * 32;
+template <typename T, int D, int NT>
+__device__ __forceinline__ void gather_weights(const Params& p, int block, int blocks, float2* s_stat) {
+    using X = Shape<T, D, NT>;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int chunks = (p.max_len + kWeightSlots - 1) / kWeightSlots;
+    const int64_t all = (int64_t)p.N * p.H * chunks;
+    for (int64_t w = block; w < all; w += blocks) {
+        const int64_t nh = w / chunks, n = nh / p.H;
+        const int j = (int)(w % chunks) * kWeightSlots + tid * 4, h = (int)(nh % p.H);
+        const int len = checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err);
+        const int64_t before = p.tiles_before[n], work = (int64_t)p.tiles_before[p.N] * p.H * p.GT;
+        if ((int)(w % chunks) * kWeightSlots >= len) continue;     // the whole block agrees
+        float* acc = p.acc + nh * p.slots + j;
+        float old[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) old[u] = j + u < len ? acc[u] : 0.f;
+        const int tiles = (len + X::kTile - 1) / X::kTile, C = split_blocks(work, p.most_blocks);
+        const int64_t seg = (before * p.H + (int64_t)h * tiles) * p.GT;        // the head's first tile
+        for (int gt = 0; gt < p.GT; ++gt) {
+            const int64_t t0 = seg + (int64_t)gt * tiles;
+            const int b0 = split_block_of(work, C, t0), k = split_block_of(work, C, t0 + tiles - 1) - b0 + 1;
+            const int heads = min(8 * NT, p.G - gt * 8 * NT);
+            // four heads' scores are on their way while the statistics are formed
+            const float* s = p.scores + (t0 + j / X::kTile) * p.GS * X::kTile + j % X::kTile;
+            float4 x[4];
+            if (j < len) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    if (g < heads) x[g] = *reinterpret_cast<const float4*>(s + g * X::kTile);
+            }
+            __syncthreads();                                       // the stats before have been read
+            for (int g = warp; g < heads; g += kJoinWarps) {       // a warp a head
+                if (k == 1) {
+                    if (lane == 0) s_stat[g] = p.stats[n * p.Hq + h * p.G + gt * 8 * NT + g];
+                    continue;
+                }
+                float m = -INFINITY, l = 0.f;                      // over the lane's parts
+                for (int i = lane; i < k; i += 32) {
+                    const float* ml = p.parts + (int64_t)(i == 0 ? 2 * b0 + 1 : 2 * (b0 + i)) * X::kPart +
+                                      X::kRegs * 32 + g;
+                    const float mi = ml[0], mn = fmaxf(m, mi), base = mn == -INFINITY ? 0.f : mn;
+                    l = l * exp2_fast(m - base) + ml[8 * NT] * exp2_fast(mi - base);
+                    m = mn;
+                }
+                float top = m;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float base = top == -INFINITY ? 0.f : top;
+                l = warp_sum(l * exp2_fast(m - base));
+                if (lane == 0) s_stat[g] = make_float2(base, l > 0.f ? 1.f / l : 0.f);
+            }
+            __syncthreads();
+            if (j >= len) continue;
+            for (int g0 = 0; g0 < heads; g0 += 4) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (g0 + g >= heads) break;
+                    const float2 t = s_stat[g0 + g];
+                    sum[0] = fmaf(exp2_fast(x[g].x - t.x), t.y, sum[0]);
+                    sum[1] = fmaf(exp2_fast(x[g].y - t.x), t.y, sum[1]);
+                    sum[2] = fmaf(exp2_fast(x[g].z - t.x), t.y, sum[2]);
+                    sum[3] = fmaf(exp2_fast(x[g].w - t.x), t.y, sum[3]);
+                    if (g0 + 4 + g < heads) x[g] = *reinterpret_cast<const float4*>(s + (g0 + 4 + g) * X::kTile);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < len) acc[u] = old[u] + sum[u];
+    }
+}
+
 // Joins the parts of every segment that spans blocks, by two kinds of work items:
 //  - up to kFew parts (many segments then): a segment; each of eight warps takes an eighth of the
 //    output registers through all parts;
 //  - more parts (one long sequence leaves a hundred to each of its heads): two registers of a
 //    segment; the warps take every eighth part. 148 parts of 2 heads: 18.6 us with items of eight
 //    registers, 9.8 us with these.
-constexpr int kJoinWarps = 8, kJoinPerSm = 4, kFew = 8;
+// The blocks from join_blocks on gather the weights instead.
 template <int NT>
 struct JoinShared {
+    float2 stat[8 * NT];
     float f[kMaxBlocks][8], l[kMaxBlocks][8];
     float few[kFew][8 * NT];
-    float sum[8], top[8];
+    float sum[8];
     float o[kJoinWarps][2][32];
     int list[kMaxBlocks], count[2][kJoinWarps];
 };
@@ -640,20 +720,17 @@ __device__ __forceinline__ void store_joined(const Params& p, int n, int head, i
     if (p.z != nullptr) v *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
     static_cast<T*>(p.o)[at] = from_f32<T>(v);
 }
-template <int NT>
-__device__ __forceinline__ void store_stats(const Params& p, int n, int head, int h, float top, float inv) {
-    const int hg = (head % p.GT) * 8 * NT + h;
-    if (p.stats != nullptr && hg < p.G)
-        p.stats[(int64_t)n * p.Hq + head / p.GT * p.G + hg] = make_float2(top, inv);
-}
-
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel(const Params p, int join_blocks) {
     using X = Shape<T, D, NT>;
     constexpr int kThreads = kJoinWarps * 32, kShare = X::kRegs / kJoinWarps, kPairs = X::kRegs / 2;
     __shared__ JoinShared<NT> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_wait();
+    if ((int)blockIdx.x >= join_blocks) {
+        gather_weights<T, D, NT>(p, blockIdx.x - join_blocks, gridDim.x - join_blocks, sh.stat);
+        return;
+    }
     // the blocks whose last segment goes on: those of few parts from the list's start, of many
     // from its end
     int few = 0, many = 0;
@@ -683,7 +760,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
     }
     auto part = [&](int b, int j) { return p.parts + (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * X::kPart; };
 
-    for (int w = blockIdx.x; w < few + many * kPairs; w += gridDim.x) {
+    for (int w = blockIdx.x; w < few + many * kPairs; w += join_blocks) {
         const bool pair = w < many * kPairs;
         const int b = pair ? sh.list[kMaxBlocks - 1 - w / kPairs] : sh.list[w - many * kPairs];
         const int4 meta = *reinterpret_cast<const int4*>(p.meta + 4 * b);
@@ -707,7 +784,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
                 const float inv = sm > 0.f ? 1.f / sm : 0.f;
 #pragma unroll
                 for (int j = 0; j < kFew; ++j) sh.few[j][tid] = m[j] * inv;
-                store_stats<NT>(p, n, head, tid, base, inv);
             }
             float x[kShare], y[kShare];
 #pragma unroll
@@ -754,7 +830,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
             sm = warp_sum(sm);
             if (lane == 0) {
                 sh.sum[warp] = sm > 0.f ? 1.f / sm : 0.f;
-                sh.top[warp] = base;
             }
         }
         __syncthreads();
@@ -776,46 +851,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
             part_coord<D>(r0 + warp, lane, h, ch);
             store_joined<T, D, NT>(p, n, head, h, ch, v * sh.sum[h & 7]);
         }
-        if (r0 % (D / 4) == 0 && tid < 8) store_stats<NT>(p, n, head, nt * 8 + tid, sh.top[tid], sh.sum[tid]);
-    }
-}
-
-// acc[n, h, j] += sum over the group's heads of exp2(score - max) / sum. Four slots a thread.
-constexpr int kWeightThreads = 128, kWeightSlots = 4 * kWeightThreads;
-template <int kTile>
-__global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(const Params p, int NT8) {
-    grid_wait();
-    const int chunks = (p.max_len + kWeightSlots - 1) / kWeightSlots;
-    const int64_t all = (int64_t)p.N * p.H * chunks;
-    for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
-        const int64_t nh = w / chunks, n = nh / p.H;
-        const int j = (int)(w % chunks) * kWeightSlots + threadIdx.x * 4, h = (int)(nh % p.H);
-        const int len = checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err);
-        const int64_t before = p.tiles_before[n];
-        if (j >= len) continue;
-        float* acc = p.acc + nh * p.slots + j;
-        float old[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) old[u] = j + u < len ? acc[u] : 0.f;
-        const int tiles = (len + kTile - 1) / kTile;
-        const int64_t tile = (before * p.H + (int64_t)h * tiles) * p.GT + j / kTile;
-        const float2* st = p.stats + n * p.Hq + h * p.G;
-        for (int gt = 0; gt < p.GT; ++gt) {
-            const float* s = p.scores + (tile + (int64_t)gt * tiles) * p.GS * kTile + j % kTile;
-            const int gs = min(NT8, p.G - gt * NT8);
-#pragma unroll 4
-            for (int g = 0; g < gs; ++g) {
-                const float2 t = st[gt * NT8 + g];
-                const float4 x = *reinterpret_cast<const float4*>(s + g * kTile);
-                sum[0] = fmaf(exp2_fast(x.x - t.x), t.y, sum[0]);
-                sum[1] = fmaf(exp2_fast(x.y - t.x), t.y, sum[1]);
-                sum[2] = fmaf(exp2_fast(x.z - t.x), t.y, sum[2]);
-                sum[3] = fmaf(exp2_fast(x.w - t.x), t.y, sum[3]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (j + u < len) acc[u] = old[u] + sum[u];
     }
 }
 
@@ -833,7 +868,7 @@ Layout layout(int64_t N, int64_t Hq, int64_t H, int64_t max_len, bool with_acc, 
     l.meta = 0;
     l.parts = up256(kMaxBlocks * 4 * sizeof(int));
     l.tiles_before = l.parts + up256(2 * kMaxBlocks * part_floats * sizeof(float));
-    l.stats = l.tiles_before + (with_acc ? up256(N * sizeof(int)) : 0);
+    l.stats = l.tiles_before + (with_acc ? up256((N + 1) * sizeof(int)) : 0);
     l.scores = l.stats + (with_acc ? up256(N * Hq * sizeof(float2)) : 0);
     const int64_t padded = (max_len + 127) / 128 * 128;          // whole tiles of 64 or 128 slots
     l.total = l.scores + (with_acc ? (size_t)(N * H * GT) * padded * GS * sizeof(float) : 0);
@@ -880,11 +915,15 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     kernel<<<p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_after(paged_join_kernel<T, D, NT>, dim3(sms * kJoinPerSm), kJoinWarps * 32, stream, p);
-    if (e != cudaSuccess || a.acc == nullptr || a.max_len == 0) return e;
-    const int64_t all = (int64_t)a.N * a.H * ((a.max_len + kWeightSlots - 1) / kWeightSlots);
-    const unsigned grid = (unsigned)(all < sms * 16 ? all : sms * 16);
-    return launch_after(paged_weights_kernel<X::kTile>, dim3(grid), kWeightThreads, stream, p, 8 * NT);
+    int join_blocks = sms * kJoinPerSm;
+    int64_t weight_blocks = 0;
+    if (a.acc != nullptr) {
+        weight_blocks = (int64_t)a.N * a.H * ((a.max_len + kWeightSlots - 1) / kWeightSlots);
+        if (weight_blocks > sms * kJoinPerSm) weight_blocks = sms * kJoinPerSm;
+        join_blocks /= 2;
+    }
+    return launch_after(paged_join_kernel<T, D, NT>, dim3(join_blocks + (unsigned)weight_blocks),
+                        kJoinWarps * 32, stream, p, join_blocks);
 }
 
 template <typename T, int D>
