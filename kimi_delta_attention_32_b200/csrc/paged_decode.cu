@@ -26,19 +26,18 @@
 //  - fp32: m16n8k8 TF32, each operand split in two (x = hi + lo, both TF32) and three products,
 //    which leaves about 2^-20 of a product at most, and 2^-22 of it on average.
 //
-// Memory. Every warp owns a ring of S stages (16 K rows and 16 V rows each), filled by 16-byte
-// cp.async and waited for by its own lanes only. 16-byte piece c of row r lies at piece c ^ (r % 8):
-// ldmatrix reads eight rows without a bank conflict. The row addresses of a tile come from the
-// block table one tile before they are used, so a load never waits for its page number. Rows
-// behind the end or with a bad page number are filled with zeros and masked.
+// Memory. Every warp owns a ring of U units (16 K rows or 16 V rows, in turn), filled by 16-byte
+// cp.async and waited for by its own lanes only: no warp waits for another between a segment's
+// first tile and its end. 16-byte piece c of row r lies at piece c ^ (r % 8): ldmatrix reads eight
+// rows without a bank conflict. The page numbers of a tile are read one tile before they are used.
+// Rows behind the end or with a bad page number are filled with zeros and masked.
 #include "decode_split.h"
 #include "paged.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kMaxBlocks = 320;          // blocks of one launch: 2 an SM, for up to 160 SMs
-constexpr int kMergeFloats = 2048;       // shared floats for joining a block's warps
+constexpr int kMaxBlocks = 480;          // blocks of one launch: 3 an SM, for up to 160 SMs
 constexpr float kSlack = 8.f;            // a score may exceed the running maximum by 2^8
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -108,27 +107,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
 // Sizes of one instantiation. NT: tiles of 8 query heads that a block works on at once.
-//  - the ring holds 96 KB of rows an SM or more in flight, beside what is being read;
-//  - two blocks of 4 warps an SM while the ring and the queries fit twice (one block's join
-//    overlaps the other's stream), else one;
-//  - a stage has room for a segment's queries, as every tile in flight may begin a segment.
+//  - two blocks of 4 warps an SM, three where a row is 128 bytes and the registers allow: a block's
+//    join of its warps then overlaps the others' streams. fp32 rows of 512 bytes leave room for one
+//    block, of 8 warps with three units each;
+//  - 96 to 160 KB of rows an SM are in flight beside what is being read;
+//  - every tile in flight, and the current one, may begin a segment: room for NQ segments' queries.
 template <typename T, int D, int NT>
 struct Shape {
+    static constexpr bool kBf16 = sizeof(T) == 2;
     static constexpr int kRowBytes = D * (int)sizeof(T);
     static constexpr int kPieces = kRowBytes / 16;               // 16-byte pieces of a row
-    static constexpr bool kWide = sizeof(T) == 2 ? D == 128 && NT > 1 : D == 64 && NT > 1;
-    static constexpr int W = kWide ? 8 : 4;
-    static constexpr int S = sizeof(T) == 2 && D == 64 ? 5 : 3;
-    static constexpr int kPerSm = kWide || (sizeof(T) == 4 && D == 128) ? 1 : 2;
+    static constexpr int W = kRowBytes == 512 ? 8 : 4;
+    static constexpr int kPerSm = kRowBytes == 512 ? 1 : kRowBytes == 128 && NT < 4 ? 3 : 2;
+    static constexpr int U = kRowBytes == 512 ? 3 : kRowBytes == 128 ? (NT < 4 ? 8 : 10) : NT < 4 ? 6 : 5;
+    static constexpr int NQ = U / 2 + 1;
     static constexpr int kTile = 16 * W;                         // slots of a tile
-    static constexpr int kStage = 32 * kRowBytes;                // a warp's K and V rows
+    static constexpr int kUnit = 16 * kRowBytes;                 // a warp's K or V rows of a tile
     static constexpr int kQ = 8 * NT * kRowBytes;                // a segment's queries
     static constexpr int kRegs = D / 4 * NT;                     // output registers a lane (D/16 x 4 x NT)
     static constexpr int kPart = kRegs * 32 + 16 * NT;           // floats of a part: O, m, l
-    static constexpr size_t kSmem = (size_t)S * (W * kStage + kQ) + kMergeFloats * 4 +
-                                    (2 * W * 8 * NT + W * S) * 4;
-    static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert(kPerSm == 1 || 2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
+    static constexpr size_t kSmem = (size_t)U * W * kUnit + NQ * kQ + (2 * W * 8 * NT + W * NQ) * 4;
+    static_assert(kSmem <= 227 * 1024 && kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
+    static_assert(D / 4 * 32 * 4 <= kUnit, "a unit holds a head tile's outputs");
 };
 
 struct Params {
@@ -162,20 +162,28 @@ __device__ __forceinline__ void part_coord(int r, int lane, int& head, int& ch) 
     ch = mt * 16 + (lane >> 2) + 8 * (c >> 1);
 }
 
+// The output of head h, channel ch of a segment (h of its head tile), from the weighted sum.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void store_joined(const Params& p, int n, int head, int h, int ch, float v) {
+    const int hg = (head % p.GT) * 8 * NT + h;
+    if (hg >= p.G) return;
+    const int64_t at = ((int64_t)n * p.Hq + head / p.GT * p.G + hg) * D + ch;
+    if (p.z != nullptr) v *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
+    static_cast<T*>(p.o)[at] = from_f32<T>(v);
+}
 // kRuns: a page holds a multiple of 16 slots, so a warp's 16 lie in one page.
 template <typename T, int D, int NT, bool kRuns>
 __global__ void __launch_bounds__(Shape<T, D, NT>::W * 32, Shape<T, D, NT>::kPerSm)
 paged_decode_kernel(const Params p) {
     using X = Shape<T, D, NT>;
-    constexpr int W = X::W, S = X::S, kThreads = W * 32, kTile = X::kTile;
-    constexpr bool kBf16 = sizeof(T) == 2;
+    constexpr int W = X::W, U = X::U, NQ = X::NQ, kThreads = W * 32, kTile = X::kTile;
+    constexpr bool kBf16 = X::kBf16;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* s_ring = smem;                                        // [W][S][K 16 rows, V 16 rows]
-    uint8_t* s_q = s_ring + (size_t)S * W * X::kStage;             // [S][8 NT rows]
-    float* s_merge = reinterpret_cast<float*>(s_q + (size_t)S * X::kQ);
-    float* s_m = s_merge + kMergeFloats;                           // [W][8 NT]
+    uint8_t* s_ring = smem;                                        // [W][U][16 rows]
+    uint8_t* s_q = s_ring + (size_t)U * W * X::kUnit;              // [NQ][8 NT rows]
+    float* s_m = reinterpret_cast<float*>(s_q + (size_t)NQ * X::kQ);    // [W][8 NT]
     float* s_l = s_m + W * 8 * NT;
-    uint32_t* s_live = reinterpret_cast<uint32_t*>(s_l + W * 8 * NT);   // [W][S] slots to attend to
+    uint32_t* s_live = reinterpret_cast<uint32_t*>(s_l + W * 8 * NT);   // [W][NQ] slots to attend to
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int heads = p.H * p.GT;                                  // segments of a sequence
@@ -272,12 +280,12 @@ paged_decode_kernel(const Params p) {
     const int own = warp * 16 + (kRuns ? 0 : lane & 15);           // the lane's slot of a tile
     const int own_page = own / p.c.page_size, own_row = own % p.c.page_size;
     int at_page = (ahead.tile * kTile + own) / p.c.page_size, row = (ahead.tile * kTile + own) % p.c.page_size;
-    int page = -1, loaded = 0, seg_loaded = -1, st_loaded = 0;
+    int page = -1, loaded = 0, seg_loaded = -1, at_unit = 0;
     auto fetch = [&]() {
         if (loaded < count && ahead.tile * kTile + own < ahead.len)
             page = __ldg(p.c.block_table + (int64_t)ahead.n * p.c.max_pages + at_page);
     };
-    uint8_t* ring = s_ring + (size_t)warp * S * X::kStage;
+    uint8_t* ring = s_ring + (size_t)warp * U * X::kUnit;
     // row a of those that a warp instruction covers, 16-byte piece `piece`; rows r0 + a lie r0 rows
     // on, with the piece's place exchanged by r0's low bits
     constexpr int kRows = 32 / X::kPieces;
@@ -286,7 +294,30 @@ paged_decode_kernel(const Params p) {
     const int64_t lane_src = (kRuns ? la * p.slot_bytes : 0) + piece * 16;
     const uint8_t* kbase = static_cast<const uint8_t*>(p.c.k) + lane_src;
     const uint8_t* vbase = static_cast<const uint8_t*>(p.c.v) + lane_src;
-    auto load = [&]() {          // tile `loaded`: its rows, and its queries if it begins a segment
+    int64_t off = 0;                                   // of the tile being loaded: its rows,
+    uint32_t mask = 0;                                 // and of the 16 slots those to attend to
+    auto load_rows = [&](const uint8_t* from_base) {
+        const uint32_t dst = lane_dst + at_unit * X::kUnit;
+        if (kRuns && mask == 0xffffu) {
+            const uint8_t* src = from_base + off;
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += kRows) {
+                cp_async16((dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4), src);
+                src += kRows * p.slot_bytes;
+            }
+        } else {
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += kRows) {
+                const bool ok = mask >> (r0 + la) & 1;
+                int64_t from = off;
+                if constexpr (kRuns) from = ok ? off + r0 * p.slot_bytes : 0;
+                else from = __shfl_sync(0xffffffffu, off, r0 + la);
+                cp_async16((dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4), from_base + from, ok);
+            }
+        }
+        if (++at_unit == U) at_unit = 0;
+    };
+    auto load_k = [&]() {        // K rows of tile `loaded`, and its queries if it begins a segment
         if (loaded < count) {
             const int hkv = p.GT == 1 ? ahead.head : ahead.head / p.GT;
             bool live = ahead.tile * kTile + own < ahead.len;
@@ -294,40 +325,17 @@ paged_decode_kernel(const Params p) {
                 atomicOr(p.c.err, kErrIndex);
                 live = false;
             }
-            uint32_t mask;                             // of the 16 slots, those to attend to
             if constexpr (kRuns) {
                 const int n = live ? min(16, ahead.len - ahead.tile * kTile - own) : 0;
                 mask = (1u << n) - 1;
             } else {
                 mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
             }
-            if (lane == 0) s_live[warp * S + st_loaded] = mask;
-            const int64_t off = live ? page * p.page_bytes + row * p.slot_bytes + hkv * p.head_bytes : 0;
-            const uint32_t dst = lane_dst + st_loaded * X::kStage;
-            if (kRuns && mask == 0xffffu) {
-                const uint8_t *k = kbase + off, *v = vbase + off;
-#pragma unroll
-                for (int r0 = 0; r0 < 16; r0 += kRows) {
-                    const uint32_t to = (dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4);
-                    cp_async16(to, k);
-                    cp_async16(to + 16 * X::kRowBytes, v);
-                    k += kRows * p.slot_bytes;
-                    v += kRows * p.slot_bytes;
-                }
-            } else {
-#pragma unroll
-                for (int r0 = 0; r0 < 16; r0 += kRows) {
-                    const uint32_t to = (dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4);
-                    const bool ok = mask >> (r0 + la) & 1;
-                    int64_t from = off;
-                    if constexpr (kRuns) from = ok ? off + r0 * p.slot_bytes : 0;
-                    else from = __shfl_sync(0xffffffffu, off, r0 + la);
-                    cp_async16(to, kbase + from, ok);
-                    cp_async16(to + 16 * X::kRowBytes, vbase + from, ok);
-                }
-            }
+            if (lane == 0) s_live[warp * NQ + loaded % NQ] = mask;
+            off = live ? page * p.page_bytes + row * p.slot_bytes + hkv * p.head_bytes : 0;
+            load_rows(kbase);
             if (loaded == 0 || ahead.tile == 0) {
-                if (++seg_loaded == S) seg_loaded = 0;
+                if (++seg_loaded == NQ) seg_loaded = 0;
                 const int gt = ahead.head - hkv * p.GT;
                 const uint32_t qd = smem_u32(s_q + (size_t)seg_loaded * X::kQ);
                 for (int e = tid; e < 8 * NT * X::kPieces; e += kThreads) {
@@ -338,7 +346,12 @@ paged_decode_kernel(const Params p) {
                                reinterpret_cast<const uint8_t*>(src) + pc * 16, ok);
                 }
             }
-            if (++st_loaded == S) st_loaded = 0;
+        }
+        cp_commit();
+    };
+    auto load_v = [&]() {        // its V rows; then on to the next tile
+        if (loaded < count) {
+            load_rows(vbase);
             if (++loaded < count) {
                 next(ahead);
                 at_page += p.step_pages;
@@ -356,9 +369,15 @@ paged_decode_kernel(const Params p) {
         }
         cp_commit();
     };
+    // the unit loaded while unit u is read is u + U - 1: of the other kind if U is even
+    auto load_at_k = [&]() { if constexpr (U % 2) load_k(); else load_v(); };
+    auto load_at_v = [&]() { if constexpr (U % 2) load_v(); else load_k(); };
     fetch();
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) load();
+    for (int u = 0; u < U - 1; ++u) {
+        if (u % 2 == 0) load_k();
+        else load_v();
+    }
 
     // ---- the tiles
     float out[NT][D / 16][4], m[NT][2], base[NT][2], l[NT][2];     // base: m, or 0 while m is -inf
@@ -375,18 +394,35 @@ paged_decode_kernel(const Params p) {
         }
     };
     reset();
-    int st = -1, st_q = 0;
+    int k_unit = 0, at_q = 0, tile_slot = 0;
+    // bf16 queries of up to 16 heads stay in registers through their segment
+    constexpr bool kHoldQ = kBf16 && NT <= 2;
+    uint32_t held_q[kHoldQ ? NT : 1][kHoldQ ? X::kPieces / 4 : 1][4];
     bool from_start = cur.tile == 0;               // the segment begins in this block
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
-        cp_wait<S - 2>();
-        __syncwarp();
-        load();                                    // into the stage read in the step before
-        if (++st == S) st = 0;
-        if (i == 0 || cur.tile == 0) __syncthreads();              // the segment's queries are there
-        const uint32_t kd = smem_u32(ring) + st * X::kStage, vd = kd + 16 * X::kRowBytes;
-        const uint32_t qd = smem_u32(s_q) + st_q * X::kQ;
-        const uint32_t mask = s_live[warp * S + st];
+        const int ar = lane & 15, ax = ar & 7, bx = lane & 7;
+        cp_wait<U - 2>();
+        // the segment's queries are there, and its predecessor's outputs have been read from the
+        // ring; otherwise the warp's own rows are all it needs
+        const bool first = i == 0 || cur.tile == 0;
+        if (first) __syncthreads();
+        else __syncwarp();
+        load_at_k();                               // into the unit read last: the tile before's V rows
+        const uint32_t kd = smem_u32(ring) + k_unit * X::kUnit;
+        const uint32_t qd = smem_u32(s_q) + at_q * X::kQ;
+        const uint32_t attend = s_live[warp * NQ + tile_slot];
+        if (++tile_slot == NQ) tile_slot = 0;
+        if constexpr (kHoldQ) {
+            if (first) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int ks = 0; ks < X::kPieces / 4; ++ks)
+                        ldsm4(qd + (nt * 8 + bx) * X::kRowBytes + (((4 * ks + (lane >> 3)) ^ bx) << 4),
+                              held_q[nt][ks]);
+            }
+        }
 
         // S^T = K Q^T: rows slots, columns heads. Several accumulators shorten the chain.
         constexpr int kAccs = kBf16 ? 2 : 3;
@@ -399,7 +435,6 @@ paged_decode_kernel(const Params p) {
 #pragma unroll
                 for (int u = 0; u < kAccs - 1; ++u) sx[u][nt][c] = 0.f;
             }
-        const int ar = lane & 15, ax = ar & 7, bx = lane & 7;
         // (fp32's 16 or 8 steps of three products and their splits are kept a loop: unrolled, the
         // tile's code no longer fits the instruction cache)
 #pragma unroll (kBf16 ? X::kPieces / 4 : 1)
@@ -410,7 +445,12 @@ paged_decode_kernel(const Params p) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 uint32_t bq[4];
-                ldsm4(qd + (nt * 8 + bx) * X::kRowBytes + (((2 * ks + (lane >> 3)) ^ bx) << 4), bq);
+                if constexpr (kHoldQ) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) bq[c] = held_q[nt][ks / 2][c];
+                } else {
+                    ldsm4(qd + (nt * 8 + bx) * X::kRowBytes + (((2 * ks + (lane >> 3)) ^ bx) << 4), bq);
+                }
                 if constexpr (kBf16) {
                     mma_bf16(s[nt], a0, bq[0], bq[1]);
                     mma_bf16(sx[0][nt], a1, bq[2], bq[3]);
@@ -420,7 +460,7 @@ paged_decode_kernel(const Params p) {
                 }
             }
         }
-        const bool ok0 = mask >> (lane >> 2) & 1, ok1 = mask >> ((lane >> 2) + 8) & 1;
+        const bool ok0 = attend >> (lane >> 2) & 1, ok1 = attend >> ((lane >> 2) + 8) & 1;
         bool above = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -471,6 +511,13 @@ paged_decode_kernel(const Params p) {
                 l[nt][c & 1] += s[nt][c];
             }
         // O^T += V^T P^T: rows channels, columns heads
+        cp_wait<U - 2>();
+        __syncwarp();
+        load_at_v();                               // into the tile's K rows
+        if (++k_unit == U) k_unit = 0;
+        const int v_unit = k_unit;
+        if (++k_unit == U) k_unit = 0;
+        const uint32_t vd = smem_u32(ring) + v_unit * X::kUnit;
         if constexpr (kBf16) {
             uint32_t pb[NT][2];
 #pragma unroll
@@ -509,7 +556,7 @@ paged_decode_kernel(const Params p) {
                         const int r = 8 * half + (lane & 3) + 4 * (c >> 1);
                         const int ch = mt * 16 + (lane >> 2) + 8 * (c & 1);
                         a[c] = *reinterpret_cast<const uint32_t*>(
-                            ring + st * X::kStage + (16 + r) * X::kRowBytes +
+                            ring + v_unit * X::kUnit + r * X::kRowBytes +
                             (((ch >> 2) ^ (r & 7)) << 4) + (ch & 3) * 4);
                     }
 #pragma unroll
@@ -532,71 +579,59 @@ paged_decode_kernel(const Params p) {
                         s_l[warp * 8 * NT + nt * 8 + 2 * lane + e] = l[nt][e];
                     }
                 }
-            __syncthreads();
             const bool whole = from_start && to_end;
             // a part that began earlier, or spans the block, is its first; one that goes on its last
             float* part = p.parts + (int64_t)(2 * b + (from_start ? 1 : 0)) * X::kPart;
-            float sum[NT][2], mul[NT][2];
+            const int gt = cur.head % p.GT, g0 = cur.head / p.GT * p.G;
+            // One tile of 8 heads after the other: the warps put their outputs where their V rows
+            // were, and each sums an eighth or a quarter of the registers, weighted by its own
+            // maximum and the block's.
+            constexpr int kRound = D / 4, kShare = kRound / W;
+            float* mine = reinterpret_cast<float*>(ring + v_unit * X::kUnit) + lane;
+            const float* theirs = reinterpret_cast<const float*>(s_ring + v_unit * X::kUnit) + lane;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                if (nt == 0) __syncwarp();         // every lane has read its V rows
+                else __syncthreads();
+#pragma unroll
+                for (int r = 0; r < kRound; ++r) mine[r * 32] = out[nt][r >> 2][r & 3];
+                __syncthreads();
+                float f[W][2], sum[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int h = nt * 8 + 2 * (lane & 3) + e;
                     float mx = -INFINITY, sm = 0.f;
 #pragma unroll
                     for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w * 8 * NT + h]);
-                    const float base = mx == -INFINITY ? 0.f : mx;
+                    const float top = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        sm += s_l[w * 8 * NT + h] * exp2_fast(s_m[w * 8 * NT + h] - base);
-                    mul[nt][e] = exp2_fast(m[nt][e] - base);
-                    sum[nt][e] = sm;
+                    for (int w = 0; w < W; ++w) {
+                        f[w][e] = exp2_fast(s_m[w * 8 * NT + h] - top);
+                        sm += s_l[w * 8 * NT + h] * f[w][e];
+                    }
+                    sum[e] = sm > 0.f ? 1.f / sm : 0.f;
                     if (warp == 0 && lane < 4) {
                         if (!whole) {
                             part[X::kRegs * 32 + h] = mx;
                             part[X::kRegs * 32 + 8 * NT + h] = sm;
-                        } else if (p.stats != nullptr && (cur.head % p.GT) * 8 * NT + h < p.G) {
-                            const int64_t at = (int64_t)cur.n * p.Hq + cur.head / p.GT * p.G +
-                                               (cur.head % p.GT) * 8 * NT + h;
-                            p.stats[at] = make_float2(base, sm > 0.f ? 1.f / sm : 0.f);
+                        } else if (p.stats != nullptr && gt * 8 * NT + h < p.G) {
+                            p.stats[(int64_t)cur.n * p.Hq + g0 + gt * 8 * NT + h] = make_float2(top, sum[e]);
                         }
                     }
                 }
-            // sum the warps' outputs, kRound registers at a time; each warp finishes its share
-            constexpr int kRound = kMergeFloats / kThreads, kShare = kRound / W;
-            static_assert(X::kRegs % kRound == 0 && kRound % W == 0, "rounds");
-            const float* flat = &out[0][0][0];
-#pragma unroll
-            for (int r0 = 0; r0 < X::kRegs; r0 += kRound) {
-                if (r0 > 0) __syncthreads();
-#pragma unroll
-                for (int r = 0; r < kRound; ++r) {
-                    const int nt = (r0 + r) / (D / 4);
-                    s_merge[(warp * kRound + r) * 32 + lane] = flat[r0 + r] * mul[nt][r & 1];
-                }
-                __syncthreads();
 #pragma unroll
                 for (int u = 0; u < kShare; ++u) {
-                    const int r = warp * kShare + u;
+                    const int r = warp * kShare + u, e = u & 1;            // (kShare is even)
                     float y = 0.f;
 #pragma unroll
-                    for (int w = 0; w < W; ++w) y += s_merge[(w * kRound + r) * 32 + lane];
+                    for (int w = 0; w < W; ++w) y += theirs[w * (U * X::kUnit / 4) + r * 32] * f[w][e];
                     if (!whole) {
-                        part[(r0 + r) * 32 + lane] = y;
-                        continue;
+                        part[(nt * kRound + r) * 32 + lane] = y;
+                    } else {
+                        int h, ch;
+                        part_coord<D>(nt * kRound + r, lane, h, ch);
+                        store_joined<T, D, NT>(p, cur.n, cur.head, h, ch, y * sum[e]);
                     }
-                    int h, ch;
-                    part_coord<D>(r0 + r, lane, h, ch);
-                    const int hg = (cur.head % p.GT) * 8 * NT + h;
-                    if (hg >= p.G) continue;
-                    const int64_t at = ((int64_t)cur.n * p.Hq + cur.head / p.GT * p.G + hg) * D + ch;
-                    float sm = 0.f;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (nt == h >> 3) sm = sum[nt][h & 1];
-                    y = sm > 0.f ? y / sm : 0.f;
-                    if (p.z != nullptr) y *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
-                    static_cast<T*>(p.o)[at] = from_f32<T>(y);
                 }
             }
             if (!whole && from_start && tid == 0) {            // this block's last: join it with the next ones'
@@ -606,7 +641,7 @@ paged_decode_kernel(const Params p) {
                 p.meta[4 * b + 2] = split_block_of(work, C, last);
             }
             reset();
-            if (++st_q == S) st_q = 0;
+            if (++at_q == NQ) at_q = 0;
             from_start = true;
         }
         if (i + 1 < count) next(cur);
@@ -711,15 +746,6 @@ struct JoinShared {
     int list[kMaxBlocks], count[2][kJoinWarps];
 };
 
-// The output of head h, channel ch of a segment (h of its head tile), from the weighted sum.
-template <typename T, int D, int NT>
-__device__ __forceinline__ void store_joined(const Params& p, int n, int head, int h, int ch, float v) {
-    const int hg = (head % p.GT) * 8 * NT + h;
-    if (hg >= p.G) return;
-    const int64_t at = ((int64_t)n * p.Hq + head / p.GT * p.G + hg) * D + ch;
-    if (p.z != nullptr) v *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
-    static_cast<T*>(p.o)[at] = from_f32<T>(v);
-}
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel(const Params p, int join_blocks) {
     using X = Shape<T, D, NT>;
