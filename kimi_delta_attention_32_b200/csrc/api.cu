@@ -130,6 +130,8 @@ kda_status fill_cache(kda::PagedCache* c, const void* k_cache, const void* v_cac
     const int64_t per16 = io == KDA_IO_BF16 ? 8 : 4;          // elements of 16 bytes
     for (int64_t s : {page_stride, slot_stride, head_stride})
         if (s < d || s % per16 != 0) return KDA_ERR_INVALID_ARG;
+    for (int64_t s : {page_stride, slot_stride, head_stride})      // counted in 16 bytes on the device
+        if (s / per16 > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     // N Hkv counts blocks, and slots rounded up to whole tiles are int32
     if ((int64_t)N * Hkv > INT32_MAX || (int64_t)max_pages * page_size > (1 << 30))
         return KDA_ERR_UNSUPPORTED;

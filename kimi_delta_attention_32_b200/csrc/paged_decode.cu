@@ -133,7 +133,7 @@ struct Shape {
 
 struct Params {
     PagedCache c;
-    int64_t page_bytes, slot_bytes, head_bytes;
+    uint32_t page16, slot16, head16; // strides in 16 bytes: their products take one instruction
     int step_pages, step_rows;       // a tile's slots, in whole pages and the rest
     const void *q, *z;
     const int32_t* seqlens;
@@ -154,23 +154,40 @@ struct Params {
     int slots;
 };
 
-// Which head, output channel a lane's register r of a part stands for (r = ((nt, mt), c)).
-template <int D>
+// Which head, output channel a lane's register r of a part stands for (r = ((nt, mt), c); c & 1 is
+// the column, c >> 1 the row). The rows of the products are channels in an order of their own: for
+// bf16 ldmatrix's, for fp32 D / 8 in a row for each of 8 groups of lanes.
+template <typename T, int D>
 __device__ __forceinline__ void part_coord(int r, int lane, int& head, int& ch) {
     const int c = r & 3, mt = (r >> 2) % (D / 16), nt = (r >> 2) / (D / 16);
     head = nt * 8 + 2 * (lane & 3) + (c & 1);
-    ch = mt * 16 + (lane >> 2) + 8 * (c >> 1);
+    ch = sizeof(T) == 2 ? mt * 16 + (lane >> 2) + 8 * (c >> 1) : (lane >> 2) * (D / 8) + 2 * mt + (c >> 1);
 }
 
-// The output of head h, channel ch of a segment (h of its head tile), from the weighted sum.
-template <typename T, int D, int NT>
-__device__ __forceinline__ void store_joined(const Params& p, int n, int head, int h, int ch, float v) {
-    const int hg = (head % p.GT) * 8 * NT + h;
-    if (hg >= p.G) return;
-    const int64_t at = ((int64_t)n * p.Hq + head / p.GT * p.G + hg) * D + ch;
-    if (p.z != nullptr) v *= sigmoid(to_f32(static_cast<const T*>(p.z)[at]));
-    static_cast<T*>(p.o)[at] = from_f32<T>(v);
+// Stores kCount of the outputs of a segment (its first query head's row is row0, of live_heads):
+// registers r0 on, of heads 2 (lane % 4) + {0, 1}, times inv of their head and the gate.
+template <typename T, int D, int NT, int kCount>
+__device__ __forceinline__ void store_out(const Params& p, int64_t row0, int live_heads, int r0, int lane,
+                                          const float (&y)[kCount], const float (&inv)[2]) {
+    float z[kCount];
+    if (p.z != nullptr) {
+#pragma unroll
+        for (int u = 0; u < kCount; ++u) {
+            int h, ch;
+            part_coord<T, D>(r0 + u, lane, h, ch);
+            z[u] = h < live_heads ? to_f32(static_cast<const T*>(p.z)[(row0 + h) * D + ch]) : 0.f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kCount; ++u) {
+        int h, ch;
+        part_coord<T, D>(r0 + u, lane, h, ch);
+        float v = y[u] * inv[u & 1];
+        if (p.z != nullptr) v *= sigmoid(z[u]);
+        if (h < live_heads) static_cast<T*>(p.o)[(row0 + h) * D + ch] = from_f32<T>(v);
+    }
 }
+
 // kRuns: a page holds a multiple of 16 slots, so a warp's 16 lie in one page.
 template <typename T, int D, int NT, bool kRuns>
 __global__ void __launch_bounds__(Shape<T, D, NT>::W * 32, Shape<T, D, NT>::kPerSm)
@@ -251,13 +268,14 @@ paged_decode_kernel(const Params p) {
         }
     }
 
-    // ---- a position in the order of tiles: sequence, head (with its head tile), tile
-    struct Cursor { int n, head, tile, len, tiles; };
-    auto next = [&](Cursor& u) {
-        if (++u.tile < u.tiles) return;
+    // ---- a position in the order of tiles: sequence, key-value head, head tile, tile
+    struct Cursor { int n, hkv, gt, tile, len, tiles; };
+    auto next_segment = [&](Cursor& u) {
         u.tile = 0;
-        if (++u.head < heads) return;
-        u.head = 0;
+        if (++u.gt < p.GT) return;
+        u.gt = 0;
+        if (++u.hkv < p.H) return;
+        u.hkv = 0;
         do {
             ++u.n;
             u.len = u.n < p.N ? len_of(u.n) : 1;
@@ -270,8 +288,10 @@ paged_decode_kernel(const Params p) {
     cur.tiles = tiles_of(cur.len);
     {
         const int64_t in_seq = t0 - (int64_t)first_before * heads;
-        cur.head = (int)(in_seq / cur.tiles);
+        const int head = (int)(in_seq / cur.tiles);
         cur.tile = (int)(in_seq % cur.tiles);
+        cur.hkv = head / p.GT;
+        cur.gt = head % p.GT;
     }
 
     // ---- loads. `ahead` is the tile whose page number is being fetched, for use when the tile is
@@ -280,10 +300,12 @@ paged_decode_kernel(const Params p) {
     const int own = warp * 16 + (kRuns ? 0 : lane & 15);           // the lane's slot of a tile
     const int own_page = own / p.c.page_size, own_row = own % p.c.page_size;
     int at_page = (ahead.tile * kTile + own) / p.c.page_size, row = (ahead.tile * kTile + own) % p.c.page_size;
-    int page = -1, loaded = 0, seg_loaded = -1, at_unit = 0;
+    int left = ahead.len - ahead.tile * kTile - own;               // slots from the lane's on
+    const int32_t* table = p.c.block_table + (int64_t)ahead.n * p.c.max_pages;
+    int page = -1, loaded = 0, seg_loaded = -1, at_unit = 0, live_slot = 0;
+    bool begins = true;                                            // the tile brings its queries
     auto fetch = [&]() {
-        if (loaded < count && ahead.tile * kTile + own < ahead.len)
-            page = __ldg(p.c.block_table + (int64_t)ahead.n * p.c.max_pages + at_page);
+        if (left > 0) page = __ldg(table + at_page);
     };
     uint8_t* ring = s_ring + (size_t)warp * U * X::kUnit;
     // row a of those that a warp instruction covers, 16-byte piece `piece`; rows r0 + a lie r0 rows
@@ -291,7 +313,8 @@ paged_decode_kernel(const Params p) {
     constexpr int kRows = 32 / X::kPieces;
     const int la = lane / X::kPieces, piece = lane % X::kPieces;
     const uint32_t lane_dst = smem_u32(ring) + la * X::kRowBytes + ((piece ^ la) << 4);
-    const int64_t lane_src = (kRuns ? la * p.slot_bytes : 0) + piece * 16;
+    const int64_t lane_src = ((kRuns ? (int64_t)la * p.slot16 : 0) + piece) * 16;
+    const int64_t rows_bytes = (int64_t)kRows * p.slot16 * 16;
     const uint8_t* kbase = static_cast<const uint8_t*>(p.c.k) + lane_src;
     const uint8_t* vbase = static_cast<const uint8_t*>(p.c.v) + lane_src;
     int64_t off = 0;                                   // of the tile being loaded: its rows,
@@ -303,14 +326,14 @@ paged_decode_kernel(const Params p) {
 #pragma unroll
             for (int r0 = 0; r0 < 16; r0 += kRows) {
                 cp_async16((dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4), src);
-                src += kRows * p.slot_bytes;
+                src += rows_bytes;
             }
         } else {
 #pragma unroll
             for (int r0 = 0; r0 < 16; r0 += kRows) {
                 const bool ok = mask >> (r0 + la) & 1;
                 int64_t from = off;
-                if constexpr (kRuns) from = ok ? off + r0 * p.slot_bytes : 0;
+                if constexpr (kRuns) from = ok ? off + r0 / kRows * rows_bytes : 0;
                 else from = __shfl_sync(0xffffffffu, off, r0 + la);
                 cp_async16((dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4), from_base + from, ok);
             }
@@ -319,31 +342,28 @@ paged_decode_kernel(const Params p) {
     };
     auto load_k = [&]() {        // K rows of tile `loaded`, and its queries if it begins a segment
         if (loaded < count) {
-            const int hkv = p.GT == 1 ? ahead.head : ahead.head / p.GT;
-            bool live = ahead.tile * kTile + own < ahead.len;
-            if (live && (page < 0 || page >= p.c.num_pages)) {
+            bool live = left > 0;
+            if (live && (unsigned)page >= (unsigned)p.c.num_pages) {
                 atomicOr(p.c.err, kErrIndex);
                 live = false;
             }
-            if constexpr (kRuns) {
-                const int n = live ? min(16, ahead.len - ahead.tile * kTile - own) : 0;
-                mask = (1u << n) - 1;
-            } else {
-                mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
-            }
-            if (lane == 0) s_live[warp * NQ + loaded % NQ] = mask;
-            off = live ? page * p.page_bytes + row * p.slot_bytes + hkv * p.head_bytes : 0;
+            mask = kRuns ? (live ? 0xffffu >> (16 - min(16, left)) : 0u)
+                         : __ballot_sync(0xffffffffu, live) & 0xffffu;
+            if (lane == 0) s_live[warp * NQ + live_slot] = mask;
+            if (++live_slot == NQ) live_slot = 0;
+            off = live ? ((uint64_t)(uint32_t)page * p.page16 + (uint64_t)(uint32_t)row * p.slot16 +
+                          (uint64_t)(uint32_t)ahead.hkv * p.head16) * 16 : 0;
             load_rows(kbase);
-            if (loaded == 0 || ahead.tile == 0) {
+            if (begins) {
                 if (++seg_loaded == NQ) seg_loaded = 0;
-                const int gt = ahead.head - hkv * p.GT;
-                const uint32_t qd = smem_u32(s_q + (size_t)seg_loaded * X::kQ);
+                const uint32_t qd = smem_u32(s_q) + seg_loaded * X::kQ;
+                const int g0 = ahead.gt * 8 * NT;
+                const T* src = q + ((int64_t)ahead.n * p.Hq + ahead.hkv * p.G + g0) * D;
                 for (int e = tid; e < 8 * NT * X::kPieces; e += kThreads) {
-                    const int g = e / X::kPieces, pc = e % X::kPieces, hg = gt * 8 * NT + g;
-                    const bool ok = hg < p.G;
-                    const T* src = q + ((int64_t)ahead.n * p.Hq + hkv * p.G + (ok ? hg : 0)) * D;
+                    const int g = e / X::kPieces, pc = e % X::kPieces;
+                    const bool ok = g0 + g < p.G;
                     cp_async16(qd + g * X::kRowBytes + ((pc ^ (g & 7)) << 4),
-                               reinterpret_cast<const uint8_t*>(src) + pc * 16, ok);
+                               reinterpret_cast<const uint8_t*>(src) + (ok ? e * 16 : 0), ok);
                 }
             }
         }
@@ -353,16 +373,22 @@ paged_decode_kernel(const Params p) {
         if (loaded < count) {
             load_rows(vbase);
             if (++loaded < count) {
-                next(ahead);
-                at_page += p.step_pages;
-                row += p.step_rows;
-                if (row >= p.c.page_size) {
-                    row -= p.c.page_size;
-                    ++at_page;
-                }
-                if (ahead.tile == 0) {
+                if (++ahead.tile < ahead.tiles) {
+                    begins = false;
+                    at_page += p.step_pages;
+                    row += p.step_rows;
+                    if (row >= p.c.page_size) {
+                        row -= p.c.page_size;
+                        ++at_page;
+                    }
+                    left -= kTile;
+                } else {
+                    next_segment(ahead);
+                    begins = true;
                     at_page = own_page;
                     row = own_row;
+                    left = ahead.len - own;
+                    table = p.c.block_table + (int64_t)ahead.n * p.c.max_pages;
                 }
                 fetch();
             }
@@ -399,13 +425,16 @@ paged_decode_kernel(const Params p) {
     constexpr bool kHoldQ = kBf16 && NT <= 2;
     uint32_t held_q[kHoldQ ? NT : 1][kHoldQ ? X::kPieces / 4 : 1][4];
     bool from_start = cur.tile == 0;               // the segment begins in this block
+    bool first = true;                             // its first tile here
+    // this lane's scores of the tile: of head h at h * kTile
+    float* scores = p.scores == nullptr ? nullptr
+                    : p.scores + t0 * p.GS * kTile + 2 * (lane & 3) * kTile + warp * 16 + (lane >> 2);
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
         const int ar = lane & 15, ax = ar & 7, bx = lane & 7;
         cp_wait<U - 2>();
         // the segment's queries are there, and its predecessor's outputs have been read from the
         // ring; otherwise the warp's own rows are all it needs
-        const bool first = i == 0 || cur.tile == 0;
         if (first) __syncthreads();
         else __syncwarp();
         load_at_k();                               // into the unit read last: the tile before's V rows
@@ -471,15 +500,14 @@ paged_decode_kernel(const Params p) {
                 s[nt][c] = (c < 2 ? ok0 : ok1) ? (s[nt][c] + sx[0][nt][c]) * p.scale_log2 : -INFINITY;
                 above |= s[nt][c] > m[nt][c & 1] + kSlack;
             }
-            if (p.scores != nullptr) {
-                float* w = p.scores + (t0 + i) * p.GS * kTile + warp * 16 + (lane >> 2);
+            if (scores != nullptr) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int g = nt * 8 + 2 * (lane & 3) + (c & 1);
-                    if (g < p.GS) w[g * kTile + 8 * (c >> 1)] = s[nt][c];
-                }
+                for (int c = 0; c < 4; ++c)
+                    if (nt * 8 + 2 * (lane & 3) + (c & 1) < p.GS)
+                        scores[(nt * 8 + (c & 1)) * kTile + 8 * (c >> 1)] = s[nt][c];
             }
         }
+        if (scores != nullptr) scores += p.GS * kTile;
         // The running maximum moves only when a score passes it by kSlack: until then the weights
         // stay below 2^kSlack, as exact as below 1, and no lane has to ask the others.
         if (__any_sync(0xffffffffu, above)) {
@@ -548,19 +576,23 @@ paged_decode_kernel(const Params p) {
                         const float v = __shfl_sync(0xffffffffu, half ? s[nt][3] : s[nt][1], from);
                         pb[nt][e] = __float_as_uint((lane >> 2) & 1 ? v : u);
                     }
+                // a lane's D / 8 channels in a row, of slots lane % 4 and 4 on: two pieces each at a
+                // time make the rows of two of the products
+                const int r = 8 * half + (lane & 3);
+                const uint8_t* v0 = ring + v_unit * X::kUnit + r * X::kRowBytes;
 #pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    uint32_t a[4];
+                for (int pc = 0; pc < D / 32; ++pc) {
+                    const int at = (lane >> 2) * (D / 32) + pc;
+                    const uint4 x = *reinterpret_cast<const uint4*>(v0 + ((at ^ (r & 7)) << 4));
+                    const uint4 y = *reinterpret_cast<const uint4*>(
+                        v0 + 4 * X::kRowBytes + ((at ^ ((r + 4) & 7)) << 4));
+                    const uint32_t a0[4] = {x.x, x.y, y.x, y.y}, a1[4] = {x.z, x.w, y.z, y.w};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {                  // channel + 8 (c & 1), slot + 4 (c >> 1)
-                        const int r = 8 * half + (lane & 3) + 4 * (c >> 1);
-                        const int ch = mt * 16 + (lane >> 2) + 8 * (c & 1);
-                        a[c] = *reinterpret_cast<const uint32_t*>(
-                            ring + v_unit * X::kUnit + r * X::kRowBytes +
-                            (((ch >> 2) ^ (r & 7)) << 4) + (ch & 3) * 4);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f32(out[nt][2 * pc], out[nt][2 * pc], out[nt][2 * pc], a0, pb[nt][0], pb[nt][1]);
+                        mma_f32(out[nt][2 * pc + 1], out[nt][2 * pc + 1], out[nt][2 * pc + 1], a1,
+                                pb[nt][0], pb[nt][1]);
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f32(out[nt][mt], out[nt][mt], out[nt][mt], a, pb[nt][0], pb[nt][1]);
                 }
             }
         }
@@ -582,7 +614,8 @@ paged_decode_kernel(const Params p) {
             const bool whole = from_start && to_end;
             // a part that began earlier, or spans the block, is its first; one that goes on its last
             float* part = p.parts + (int64_t)(2 * b + (from_start ? 1 : 0)) * X::kPart;
-            const int gt = cur.head % p.GT, g0 = cur.head / p.GT * p.G;
+            const int64_t row0 = (int64_t)cur.n * p.Hq + cur.hkv * p.G + cur.gt * 8 * NT;   // of q, z, o
+            const int live_heads = p.G - cur.gt * 8 * NT;
             // One tile of 8 heads after the other: the warps put their outputs where their V rows
             // were, and each sums an eighth or a quarter of the registers, weighted by its own
             // maximum and the block's.
@@ -614,37 +647,39 @@ paged_decode_kernel(const Params p) {
                         if (!whole) {
                             part[X::kRegs * 32 + h] = mx;
                             part[X::kRegs * 32 + 8 * NT + h] = sm;
-                        } else if (p.stats != nullptr && gt * 8 * NT + h < p.G) {
-                            p.stats[(int64_t)cur.n * p.Hq + g0 + gt * 8 * NT + h] = make_float2(top, sum[e]);
+                        } else if (p.stats != nullptr && h < live_heads) {
+                            p.stats[row0 + h] = make_float2(top, sum[e]);
                         }
                     }
                 }
+                float y[kShare];
 #pragma unroll
                 for (int u = 0; u < kShare; ++u) {
-                    const int r = warp * kShare + u, e = u & 1;            // (kShare is even)
-                    float y = 0.f;
+                    const int r = warp * kShare + u;
+                    y[u] = 0.f;
 #pragma unroll
-                    for (int w = 0; w < W; ++w) y += theirs[w * (U * X::kUnit / 4) + r * 32] * f[w][e];
-                    if (!whole) {
-                        part[(nt * kRound + r) * 32 + lane] = y;
-                    } else {
-                        int h, ch;
-                        part_coord<D>(nt * kRound + r, lane, h, ch);
-                        store_joined<T, D, NT>(p, cur.n, cur.head, h, ch, y * sum[e]);
-                    }
+                    for (int w = 0; w < W; ++w) y[u] += theirs[w * (U * X::kUnit / 4) + r * 32] * f[w][u & 1];
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int u = 0; u < kShare; ++u) part[(nt * kRound + warp * kShare + u) * 32 + lane] = y[u];
+                } else {
+                    store_out<T, D, NT, kShare>(p, row0, live_heads, nt * kRound + warp * kShare, lane, y, sum);
                 }
             }
             if (!whole && from_start && tid == 0) {            // this block's last: join it with the next ones'
                 const int64_t last = t0 + i + (cur.tiles - 1 - cur.tile);
                 p.meta[4 * b] = cur.n;
-                p.meta[4 * b + 1] = cur.head;
+                p.meta[4 * b + 1] = cur.hkv * p.GT + cur.gt;
                 p.meta[4 * b + 2] = split_block_of(work, C, last);
             }
             reset();
             if (++at_q == NQ) at_q = 0;
             from_start = true;
         }
-        if (i + 1 < count) next(cur);
+        first = to_end;
+        if (!to_end) ++cur.tile;
+        else if (i + 1 < count) next_segment(cur);
     }
     cp_wait<0>();
     grid_release();
@@ -790,7 +825,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
         const bool pair = w < many * kPairs;
         const int b = pair ? sh.list[kMaxBlocks - 1 - w / kPairs] : sh.list[w - many * kPairs];
         const int4 meta = *reinterpret_cast<const int4*>(p.meta + 4 * b);
-        const int n = meta.x, head = meta.y, k = meta.z - b + 1;
+        const int n = meta.x, hkv = meta.y / p.GT, gt = meta.y % p.GT, k = meta.z - b + 1;
+        const int64_t row0 = (int64_t)n * p.Hq + hkv * p.G + gt * 8 * NT;
+        const int live_heads = p.G - gt * 8 * NT;
+        const float ones[2] = {1.f, 1.f};
         __syncthreads();                       // the item before has been read
         if (!pair) {
             if (tid < 8 * NT) {                // factors exp2(m - max) / sum of each part
@@ -823,16 +861,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
 #pragma unroll
                 for (int r = 0; r < kShare; ++r) {
                     int h, ch;
-                    part_coord<D>(warp * kShare + r, lane, h, ch);
+                    part_coord<T, D>(warp * kShare + r, lane, h, ch);
                     y[r] += x[r] * sh.few[j][h];
                 }
             }
-#pragma unroll
-            for (int r = 0; r < kShare; ++r) {
-                int h, ch;
-                part_coord<D>(warp * kShare + r, lane, h, ch);
-                store_joined<T, D, NT>(p, n, head, h, ch, y[r]);
-            }
+            store_out<T, D, NT, kShare>(p, row0, live_heads, warp * kShare, lane, y, ones);
             continue;
         }
         const int r0 = w % kPairs * 2, nt = r0 / (D / 4);
@@ -874,8 +907,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
 #pragma unroll
             for (int u = 0; u < kJoinWarps; ++u) v += sh.o[u][warp][lane];
             int h, ch;
-            part_coord<D>(r0 + warp, lane, h, ch);
-            store_joined<T, D, NT>(p, n, head, h, ch, v * sh.sum[h & 7]);
+            part_coord<T, D>(r0 + warp, lane, h, ch);
+            const float one[1] = {v * sh.sum[h & 7]};
+            store_out<T, D, NT, 1>(p, row0, live_heads, r0 + warp, lane, one, ones);
         }
     }
 }
@@ -910,9 +944,9 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     Params p;
     p.c = a.c;
-    p.page_bytes = a.c.page_stride * (int64_t)sizeof(T);
-    p.slot_bytes = a.c.slot_stride * (int64_t)sizeof(T);
-    p.head_bytes = a.c.head_stride * (int64_t)sizeof(T);
+    p.page16 = (uint32_t)(a.c.page_stride * (int64_t)sizeof(T) / 16);
+    p.slot16 = (uint32_t)(a.c.slot_stride * (int64_t)sizeof(T) / 16);
+    p.head16 = (uint32_t)(a.c.head_stride * (int64_t)sizeof(T) / 16);
     p.step_pages = X::kTile / a.c.page_size;
     p.step_rows = X::kTile % a.c.page_size;
     p.q = a.q; p.z = a.z;
