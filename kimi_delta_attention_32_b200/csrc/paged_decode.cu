@@ -29,7 +29,7 @@
 // Memory. Every warp owns a ring of U units (16 K rows or 16 V rows, in turn), filled by 16-byte
 // cp.async and waited for by its own lanes only: no warp waits for another between a segment's
 // first tile and its end. 16-byte piece c of row r lies at piece c ^ (r % 8): ldmatrix reads eight
-// rows without a bank conflict. The page numbers of a tile are read one tile before they are used.
+// rows without a bank conflict. Page numbers are read two tiles before their rows are.
 // Rows behind the end or with a bad page number are filled with zeros and masked.
 #include "decode_split.h"
 #include "paged.cuh"
@@ -164,20 +164,24 @@ __device__ __forceinline__ void part_coord(int r, int lane, int& head, int& ch) 
     ch = sizeof(T) == 2 ? mt * 16 + (lane >> 2) + 8 * (c >> 1) : (lane >> 2) * (D / 8) + 2 * mt + (c >> 1);
 }
 
-// Stores kCount of the outputs of a segment (its first query head's row is row0, of live_heads):
-// registers r0 on, of heads 2 (lane % 4) + {0, 1}, times inv of their head and the gate.
-template <typename T, int D, int NT, int kCount>
-__device__ __forceinline__ void store_out(const Params& p, int64_t row0, int live_heads, int r0, int lane,
-                                          const float (&y)[kCount], const float (&inv)[2]) {
-    float z[kCount];
-    if (p.z != nullptr) {
+// kCount of the outputs of a segment (its first query head's row is row0, of live_heads): registers
+// r0 on, of heads 2 (lane % 4) + {0, 1}. load_gate reads their z, store_out stores them, times inv
+// of their head and sigmoid(z).
+template <typename T, int D, int kCount>
+__device__ __forceinline__ void load_gate(const Params& p, int64_t row0, int live_heads, int r0, int lane,
+                                          float (&z)[kCount]) {
+    if (p.z == nullptr) return;
 #pragma unroll
-        for (int u = 0; u < kCount; ++u) {
-            int h, ch;
-            part_coord<T, D>(r0 + u, lane, h, ch);
-            z[u] = h < live_heads ? to_f32(static_cast<const T*>(p.z)[(row0 + h) * D + ch]) : 0.f;
-        }
+    for (int u = 0; u < kCount; ++u) {
+        int h, ch;
+        part_coord<T, D>(r0 + u, lane, h, ch);
+        z[u] = h < live_heads ? to_f32(static_cast<const T*>(p.z)[(row0 + h) * D + ch]) : 0.f;
     }
+}
+template <typename T, int D, int kCount>
+__device__ __forceinline__ void store_out(const Params& p, int64_t row0, int live_heads, int r0, int lane,
+                                          const float (&y)[kCount], const float (&z)[kCount],
+                                          const float (&inv)[2]) {
 #pragma unroll
     for (int u = 0; u < kCount; ++u) {
         int h, ch;
@@ -247,7 +251,7 @@ paged_decode_kernel(const Params p) {
     }
     const int64_t t0 = split_begin(work, C, b);
     const int count = (int)(split_begin(work, C, b + 1) - t0);
-    const int target = (int)(t0 / heads);              // tiles of earlier sequences <= target
+    const int target = (int)split_div(t0, heads);      // tiles of earlier sequences <= target
     int first_n, first_before;
     {
         const int owner = __ffs(__ballot_sync(0xffffffffu, mine > 0 && target < incl)) - 1;
@@ -288,24 +292,42 @@ paged_decode_kernel(const Params p) {
     cur.tiles = tiles_of(cur.len);
     {
         const int64_t in_seq = t0 - (int64_t)first_before * heads;
-        const int head = (int)(in_seq / cur.tiles);
-        cur.tile = (int)(in_seq % cur.tiles);
+        const int head = (int)split_div(in_seq, cur.tiles);
+        cur.tile = (int)(in_seq - (int64_t)head * cur.tiles);
         cur.hkv = head / p.GT;
         cur.gt = head % p.GT;
     }
 
-    // ---- loads. `ahead` is the tile whose page number is being fetched, for use when the tile is
-    // loaded a step later: with kRuns of the warp's 16 slots, else lanes l and l + 16 of slot l's.
-    Cursor ahead = cur;
+    // ---- page numbers: with kRuns one for the warp's 16 slots of a tile, else lanes l and l + 16
+    // hold slot l's. That of the tile behind the next is on its way while the next one's is used; the
+    // heads of a sequence walk the same table, so only a new sequence starts without one.
+    Cursor ahead = cur;                                            // the tile to be loaded next
     const int own = warp * 16 + (kRuns ? 0 : lane & 15);           // the lane's slot of a tile
-    const int own_page = own / p.c.page_size, own_row = own % p.c.page_size;
-    int at_page = (ahead.tile * kTile + own) / p.c.page_size, row = (ahead.tile * kTile + own) % p.c.page_size;
+    const int own_page = own / p.c.page_size, own_row = own - own_page * p.c.page_size;
+    int at_page = (ahead.tile * kTile + own) / p.c.page_size;
+    int row = ahead.tile * kTile + own - at_page * p.c.page_size;
     int left = ahead.len - ahead.tile * kTile - own;               // slots from the lane's on
     const int32_t* table = p.c.block_table + (int64_t)ahead.n * p.c.max_pages;
-    int page = -1, loaded = 0, seg_loaded = -1, at_unit = 0, live_slot = 0;
+    int page = left > 0 ? __ldg(table + at_page) : -1, page_behind = -1;
+    int loaded = 0, seg_loaded = -1, at_unit = 0, live_slot = 0;
     bool begins = true;                                            // the tile brings its queries
-    auto fetch = [&]() {
-        if (left > 0) page = __ldg(table + at_page);
+    // the first touch of a sequence's table would stall a tile for its trip to memory
+    auto warm_table = [&]() {
+        if (warp == 0) {
+            const int e = at_page + lane * 32;
+            if (e * (int64_t)p.c.page_size < ahead.len)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(table + e));
+            if (lane == 0 && ahead.n + 1 < p.N)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(table + p.c.max_pages));
+        }
+    };
+    auto fetch_behind = [&]() {
+        if (ahead.tile + 1 < ahead.tiles) {
+            if (left > kTile)
+                page_behind = __ldg(table + at_page + p.step_pages + (row + p.step_rows >= p.c.page_size));
+        } else if ((ahead.gt + 1 < p.GT || ahead.hkv + 1 < p.H) && own < ahead.len) {
+            page_behind = __ldg(table + own_page);
+        }
     };
     uint8_t* ring = s_ring + (size_t)warp * U * X::kUnit;
     // row a of those that a warp instruction covers, 16-byte piece `piece`; rows r0 + a lie r0 rows
@@ -322,12 +344,14 @@ paged_decode_kernel(const Params p) {
     auto load_rows = [&](const uint8_t* from_base) {
         const uint32_t dst = lane_dst + at_unit * X::kUnit;
         if (kRuns && mask == 0xffffu) {
-            const uint8_t* src = from_base + off;
+            // (each load has an address register of its own: one that is reused waits for the load
+            // before it to have read it)
+            const uint8_t* src[16 / kRows];
 #pragma unroll
-            for (int r0 = 0; r0 < 16; r0 += kRows) {
-                cp_async16((dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4), src);
-                src += rows_bytes;
-            }
+            for (int i = 0; i < 16 / kRows; ++i) src[i] = from_base + off + i * rows_bytes;
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += kRows)
+                cp_async16((dst + r0 * X::kRowBytes) ^ ((r0 & 7) << 4), src[r0 / kRows]);
         } else {
 #pragma unroll
             for (int r0 = 0; r0 < 16; r0 += kRows) {
@@ -373,24 +397,30 @@ paged_decode_kernel(const Params p) {
         if (loaded < count) {
             load_rows(vbase);
             if (++loaded < count) {
+                page = page_behind;
                 if (++ahead.tile < ahead.tiles) {
                     begins = false;
-                    at_page += p.step_pages;
                     row += p.step_rows;
+                    at_page += p.step_pages;
                     if (row >= p.c.page_size) {
                         row -= p.c.page_size;
                         ++at_page;
                     }
                     left -= kTile;
                 } else {
+                    const int n = ahead.n;
                     next_segment(ahead);
                     begins = true;
-                    at_page = own_page;
                     row = own_row;
+                    at_page = own_page;
                     left = ahead.len - own;
-                    table = p.c.block_table + (int64_t)ahead.n * p.c.max_pages;
+                    if (ahead.n != n) {
+                        table = p.c.block_table + (int64_t)ahead.n * p.c.max_pages;
+                        if (left > 0) page = __ldg(table + own_page);
+                        warm_table();
+                    }
                 }
-                fetch();
+                fetch_behind();
             }
         }
         cp_commit();
@@ -398,7 +428,8 @@ paged_decode_kernel(const Params p) {
     // the unit loaded while unit u is read is u + U - 1: of the other kind if U is even
     auto load_at_k = [&]() { if constexpr (U % 2) load_k(); else load_v(); };
     auto load_at_v = [&]() { if constexpr (U % 2) load_v(); else load_k(); };
-    fetch();
+    fetch_behind();
+    warm_table();
 #pragma unroll
     for (int u = 0; u < U - 1; ++u) {
         if (u % 2 == 0) load_k();
@@ -628,6 +659,8 @@ paged_decode_kernel(const Params p) {
                 else __syncthreads();
 #pragma unroll
                 for (int r = 0; r < kRound; ++r) mine[r * 32] = out[nt][r >> 2][r & 3];
+                float z[kShare];
+                if (whole) load_gate<T, D, kShare>(p, row0, live_heads, nt * kRound + warp * kShare, lane, z);
                 __syncthreads();
                 float f[W][2], sum[2];
 #pragma unroll
@@ -664,7 +697,7 @@ paged_decode_kernel(const Params p) {
 #pragma unroll
                     for (int u = 0; u < kShare; ++u) part[(nt * kRound + warp * kShare + u) * 32 + lane] = y[u];
                 } else {
-                    store_out<T, D, NT, kShare>(p, row0, live_heads, nt * kRound + warp * kShare, lane, y, sum);
+                    store_out<T, D, kShare>(p, row0, live_heads, nt * kRound + warp * kShare, lane, y, z, sum);
                 }
             }
             if (!whole && from_start && tid == 0) {            // this block's last: join it with the next ones'
@@ -778,7 +811,8 @@ struct JoinShared {
     float few[kFew][8 * NT];
     float sum[8];
     float o[kJoinWarps][2][32];
-    int list[kMaxBlocks], count[2][kJoinWarps];
+    int4 list[kMaxBlocks];                     // n, head, last block, first block
+    int count[(kMaxBlocks + kJoinWarps * 32 - 1) / (kJoinWarps * 32)][2][kJoinWarps];
 };
 
 template <typename T, int D, int NT>
@@ -794,38 +828,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
     }
     // the blocks whose last segment goes on: those of few parts from the list's start, of many
     // from its end
+    constexpr int kEach = (kMaxBlocks + kThreads - 1) / kThreads;
+    int4 meta[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int b = i * kThreads + tid;
+        meta[i] = make_int4(0, 0, -1, 0);
+        if (b < p.most_blocks) meta[i] = *reinterpret_cast<const int4*>(p.meta + 4 * b);
+        meta[i].w = b;
+    }
     int few = 0, many = 0;
-    for (int b0 = 0; b0 < p.most_blocks; b0 += kThreads) {
-        const int b = b0 + tid;
-        const int last = b < p.most_blocks ? p.meta[4 * b + 2] : -1;
-        const bool is_few = last >= 0 && last - b + 1 <= kFew, is_many = last >= 0 && !is_few;
-        const unsigned mf = __ballot_sync(0xffffffffu, is_few), mm = __ballot_sync(0xffffffffu, is_many);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const bool open = meta[i].z >= 0, is_few = open && meta[i].z - meta[i].w < kFew;
+        const unsigned mf = __ballot_sync(0xffffffffu, is_few), mm = __ballot_sync(0xffffffffu, open && !is_few);
         if (lane == 0) {
-            sh.count[0][warp] = __popc(mf);
-            sh.count[1][warp] = __popc(mm);
+            sh.count[i][0][warp] = __popc(mf);
+            sh.count[i][1][warp] = __popc(mm);
         }
         __syncthreads();
         int at_few = few + __popc(mf & ((1u << lane) - 1)), at_many = many + __popc(mm & ((1u << lane) - 1));
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
             if (w < warp) {
-                at_few += sh.count[0][w];
-                at_many += sh.count[1][w];
+                at_few += sh.count[i][0][w];
+                at_many += sh.count[i][1][w];
             }
-            few += sh.count[0][w];
-            many += sh.count[1][w];
+            few += sh.count[i][0][w];
+            many += sh.count[i][1][w];
         }
-        if (is_few) sh.list[at_few] = b;
-        if (is_many) sh.list[kMaxBlocks - 1 - at_many] = b;
-        __syncthreads();
+        if (open) sh.list[is_few ? at_few : kMaxBlocks - 1 - at_many] = meta[i];
     }
+    __syncthreads();
     auto part = [&](int b, int j) { return p.parts + (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * X::kPart; };
 
     for (int w = blockIdx.x; w < few + many * kPairs; w += join_blocks) {
         const bool pair = w < many * kPairs;
-        const int b = pair ? sh.list[kMaxBlocks - 1 - w / kPairs] : sh.list[w - many * kPairs];
-        const int4 meta = *reinterpret_cast<const int4*>(p.meta + 4 * b);
-        const int n = meta.x, hkv = meta.y / p.GT, gt = meta.y % p.GT, k = meta.z - b + 1;
+        const int4 open = pair ? sh.list[kMaxBlocks - 1 - w / kPairs] : sh.list[w - many * kPairs];
+        const int n = open.x, hkv = open.y / p.GT, gt = open.y % p.GT, b = open.w, k = open.z - b + 1;
         const int64_t row0 = (int64_t)n * p.Hq + hkv * p.G + gt * 8 * NT;
         const int live_heads = p.G - gt * 8 * NT;
         const float ones[2] = {1.f, 1.f};
@@ -849,7 +889,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
 #pragma unroll
                 for (int j = 0; j < kFew; ++j) sh.few[j][tid] = m[j] * inv;
             }
-            float x[kShare], y[kShare];
+            float x[kShare], y[kShare], z[kShare];
+            load_gate<T, D, kShare>(p, row0, live_heads, warp * kShare, lane, z);
 #pragma unroll
             for (int r = 0; r < kShare; ++r) y[r] = 0.f;
             __syncthreads();
@@ -865,10 +906,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
                     y[r] += x[r] * sh.few[j][h];
                 }
             }
-            store_out<T, D, NT, kShare>(p, row0, live_heads, warp * kShare, lane, y, ones);
+            store_out<T, D, kShare>(p, row0, live_heads, warp * kShare, lane, y, z, ones);
             continue;
         }
         const int r0 = w % kPairs * 2, nt = r0 / (D / 4);
+        float z[1];
+        if (warp < 2) load_gate<T, D, 1>(p, row0, live_heads, r0 + warp, lane, z);
         for (int e = tid; e < k * 8; e += kThreads) {
             const float* ml = part(b, e >> 3) + X::kRegs * 32 + nt * 8 + (e & 7);
             sh.f[e >> 3][e & 7] = ml[0];
@@ -893,7 +936,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
         }
         __syncthreads();
         float y0 = 0.f, y1 = 0.f;
-#pragma unroll 8
+#pragma unroll 16
         for (int j = warp; j < k; j += kJoinWarps) {
             const float* src = part(b, j) + r0 * 32 + lane;
             y0 += src[0] * sh.f[j][2 * (lane & 3)];
@@ -909,7 +952,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
             int h, ch;
             part_coord<T, D>(r0 + warp, lane, h, ch);
             const float one[1] = {v * sh.sum[h & 7]};
-            store_out<T, D, NT, 1>(p, row0, live_heads, r0 + warp, lane, one, ones);
+            store_out<T, D, 1>(p, row0, live_heads, r0 + warp, lane, one, z, ones);
         }
     }
 }
