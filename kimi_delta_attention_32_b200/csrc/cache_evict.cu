@@ -52,7 +52,7 @@ struct SelectArgs {
 
 // kMany: the cluster has more than one block.
 template <int kThreads, bool kMany>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs s) {
+__global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 1536 / kThreads) evict_select_kernel(const SelectArgs s) {
     extern __shared__ __align__(16) uint32_t s_keys[];
     constexpr int kWarps = kThreads / 32, kAhead = 8;    // kAhead: entries a thread loads at once
     __shared__ int s_hist[3][kBins], s_coarse[3][kBins / 32];
@@ -417,13 +417,18 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     // caches take fewer threads: fewer meet at the barriers, and more blocks share an SM.
     int cluster = 1;
     while (cluster < kMaxCluster && (int64_t)cluster * 8192 < a.max_len) cluster *= 2;
-    const int threads = a.max_len <= 2048 ? 256 : cluster == 1 ? 512 : 1024;
+    // A long cache alone takes all the threads that a block can have; where more blocks than SMs are
+    // to run, blocks of 512 share an SM, and one's barriers overlap another's work (32 sequences of
+    // 32768, 8 heads: 508 us with 1024 threads, 452 us with 512).
+    const bool crowd = (int64_t)a.N * a.H * cluster > sm_count();
+    const int threads = a.max_len <= 2048 ? 256 : cluster == 1 || crowd ? 512 : 1024;
     const int block = threads / 32 * kRun;               // a block's slots come in whole runs of its warps
     const int64_t need = ((int64_t)a.max_len + cluster * block - 1) / (cluster * block) * block;
     s.keys = need <= kMaxKeys ? (int)need : 0;
     const size_t smem = (size_t)s.keys * 4;
     const cudaError_t e = threads == 256   ? launch_select<256, false>(s, 1, smem, stream)
-                          : threads == 512 ? launch_select<512, false>(s, 1, smem, stream)
+                          : cluster == 1   ? launch_select<512, false>(s, 1, smem, stream)
+                          : threads == 512 ? launch_select<512, true>(s, cluster, smem, stream)
                                            : launch_select<1024, true>(s, cluster, smem, stream);
     if (e != cudaSuccess) return e;
     const int esz = a.io == Io::BF16 ? 2 : 4;
