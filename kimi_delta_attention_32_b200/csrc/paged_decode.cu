@@ -210,10 +210,11 @@ paged_decode_kernel(const Params p) {
     const int heads = p.H * p.GT;                                  // segments of a sequence
     const T* q = static_cast<const T*>(p.q);
 
-    // ---- the block's range of tiles. Every warp finds it on its own: lane l sums the tiles of N / 32
-    // sequences, and the 32 sums tell whose sequences hold the first tile.
+    // ---- the block's range of tiles. Up to 32 sequences every warp scans their tiles on its own;
+    // more are summed by groups first, the warps sharing them, in the ring that is still empty.
     auto len_of = [&](int n) { return checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err); };
     auto tiles_of = [&](int len) { return (len + kTile - 1) / kTile; };
+    auto tiles_at = [&](int n, int end) { return n < end ? tiles_of(len_of(n)) : 0; };
     auto warp_scan = [&](int x) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -222,10 +223,27 @@ paged_decode_kernel(const Params p) {
         }
         return x;
     };
-    const int per = (p.N + 31) / 32, own0 = min(p.N, lane * per), own1 = min(p.N, own0 + per);
-    int mine = 0;
-#pragma unroll 4
-    for (int n = own0; n < own1; ++n) mine += tiles_of(len_of(n));
+    // a group is 32 sequences, or as many more as keep the groups' sums within 4096
+    const bool grouped = p.N > 32;
+    const int group = 32 * ((p.N + 32 * 4096 - 1) / (32 * 4096)), groups = (p.N + group - 1) / group;
+    int* s_sum = reinterpret_cast<int*>(smem);
+    int mine = 0, own0 = 0, own1 = 0;                  // lane l's sequences, or its groups
+    if (grouped) {
+#pragma unroll 8
+        for (int g = warp; g < groups; g += W) {
+            int x = 0;
+            for (int n = g * group + lane; n < (g + 1) * group; n += 32) x += tiles_at(n, p.N);
+            x = __reduce_add_sync(0xffffffffu, x);
+            if (lane == 0) s_sum[g] = x;
+        }
+        __syncthreads();
+        const int per = (groups + 31) / 32;
+        own0 = min(groups, lane * per);
+        own1 = min(groups, own0 + per);
+        for (int g = own0; g < own1; ++g) mine += s_sum[g];
+    } else {
+        mine = tiles_at(lane, p.N);
+    }
     const int incl = warp_scan(mine);
     const int64_t work = (int64_t)__shfl_sync(0xffffffffu, incl, 31) * heads;
     const int C = split_blocks(work, p.most_blocks), b = blockIdx.x;
@@ -237,30 +255,38 @@ paged_decode_kernel(const Params p) {
                     static_cast<T*>(p.o)[(int64_t)n * p.Hq * D + e] = from_f32<T>(0.f);
     };
     if (tid == 0) p.meta[4 * b + 2] = -1;
-    if (b == 0 && warp == 0 && p.tiles_before != nullptr) {
-        int run = incl - mine;
-        for (int n = own0; n < own1; ++n) {
-            p.tiles_before[n] = run;
-            run += tiles_of(len_of(n));
-        }
-        if (lane == 31) p.tiles_before[p.N] = incl;
-    }
     if (b >= C) {
         write_empty();
         return;
     }
+    if (p.tiles_before != nullptr && warp == 0) {
+        if (b == 0 && lane == 31) p.tiles_before[p.N] = incl;
+        if (!grouped) {
+            if (b == 0 && lane < p.N) p.tiles_before[lane] = incl - mine;
+        } else {
+            for (int g = b; g < groups; g += C) {
+                int run = 0;
+                for (int i = lane; i < g; i += 32) run += s_sum[i];
+                run = __reduce_add_sync(0xffffffffu, run);
+                for (int n = g * group + lane; n - lane < min(p.N, (g + 1) * group); n += 32) {
+                    const int x = tiles_at(n, p.N), upto = warp_scan(x);
+                    if (n < p.N) p.tiles_before[n] = run + upto - x;
+                    run += __shfl_sync(0xffffffffu, upto, 31);
+                }
+            }
+        }
+    }
     const int64_t t0 = split_begin(work, C, b);
     const int count = (int)(split_begin(work, C, b + 1) - t0);
     const int target = (int)split_div(t0, heads);      // tiles of earlier sequences <= target
-    int first_n, first_before;
-    {
-        const int owner = __ffs(__ballot_sync(0xffffffffu, mine > 0 && target < incl)) - 1;
-        first_n = owner * per;
-        first_before = __shfl_sync(0xffffffffu, incl - mine, owner);
-        const int end = min(p.N, first_n + per);
-        while (per > 1) {
-            const int x = first_n + lane < end ? tiles_of(len_of(first_n + lane)) : 0;
-            const int upto = first_before + warp_scan(x);
+    const int owner = __ffs(__ballot_sync(0xffffffffu, mine > 0 && target < incl)) - 1;
+    int first_n = owner, first_before = __shfl_sync(0xffffffffu, incl - mine, owner);
+    if (grouped) {
+        int g = __shfl_sync(0xffffffffu, own0, owner);
+        while (target >= first_before + s_sum[g]) first_before += s_sum[g++];
+        first_n = g * group;
+        while (true) {
+            const int x = tiles_at(first_n + lane, p.N), upto = first_before + warp_scan(x);
             const unsigned here = __ballot_sync(0xffffffffu, x > 0 && target < upto);
             if (here != 0) {
                 first_n += __ffs(here) - 1;
@@ -270,6 +296,7 @@ paged_decode_kernel(const Params p) {
             first_before = __shfl_sync(0xffffffffu, upto, 31);
             first_n += 32;
         }
+        __syncthreads();                               // the sums have been read: the ring may fill
     }
 
     // ---- a position in the order of tiles: sequence, key-value head, head tile, tile

@@ -143,6 +143,14 @@ def test_decode_many_sequences():
     decode_case("bf16", [int(x) for x in g.integers(0, 40, 700)], 4, 2, 64, 16, acc=True, seed=1)
 
 
+@pytest.mark.parametrize("N", [31, 32, 33, 64, 65, 1100, 5000])
+def test_decode_batch_sizes(N):
+    """Around the 32 sequences that a warp scans at once, and many of them, empty runs among them."""
+    g = np.random.default_rng(N)
+    lens = [0 if 10 <= i < 50 and N > 64 else int(x) for i, x in enumerate(g.integers(0, 70, N))]
+    decode_case("f32", lens, 2, 1, 64, 16, acc=True, seed=N)
+
+
 def test_decode_only_empty_sequences():
     c = Paged("bf16", [0, 0, 0], 2, 128, 16)
     q = c.rand(3, 4, 128)
@@ -422,7 +430,8 @@ def test_evict_positions():
 
 @pytest.mark.parametrize("length,keep", [(5000, 4096), (4097, 4096), (70000, 30000), (70000, 69990),
                                          (70000, 3), (1025, 1000), (2048, 700), (2049, 700),
-                                         (8193, 4000), (17000, 9000), (262145, 100000)])
+                                         (8193, 4000), (17000, 9000), (262145, 100000),
+                                         (390000, 200000)])
 def test_evict_long(length, keep):
     c = Paged("bf16", [length, length // 2, 10], 1, 64, 64, seed=length)
     evict_case(c, keep, 2 if keep > 3 else 0, keep // 4)
