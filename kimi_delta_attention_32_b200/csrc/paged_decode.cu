@@ -825,8 +825,8 @@ __device__ __forceinline__ void gather_weights(const Params& p, int block, int b
 }
 
 // Joins the parts of every segment that spans blocks, by two kinds of work items:
-//  - up to kFew parts (many segments then): a segment; each of eight warps takes an eighth of the
-//    output registers through all parts;
+//  - up to kFew parts (many segments then): a tile of 8 heads of a segment; each of eight warps
+//    takes an eighth of its output registers, of all parts at once;
 //  - more parts (one long sequence leaves a hundred to each of its heads): two registers of a
 //    segment; the warps take every eighth part. 148 parts of 2 heads: 18.6 us with items of eight
 //    registers, 9.8 us with these.
@@ -835,7 +835,7 @@ template <int NT>
 struct JoinShared {
     float2 stat[8 * NT];
     float f[kMaxBlocks][8], l[kMaxBlocks][8];
-    float few[kFew][8 * NT];
+    float few[kFew][8];
     float sum[8];
     float o[kJoinWarps][2][32];
     int4 list[kMaxBlocks];                     // n, head, last block, first block
@@ -845,7 +845,7 @@ struct JoinShared {
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel(const Params p, int join_blocks) {
     using X = Shape<T, D, NT>;
-    constexpr int kThreads = kJoinWarps * 32, kShare = X::kRegs / kJoinWarps, kPairs = X::kRegs / 2;
+    constexpr int kThreads = kJoinWarps * 32, kShare = D / 4 / kJoinWarps, kPairs = X::kRegs / 2;
     __shared__ JoinShared<NT> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_wait();
@@ -889,21 +889,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
     __syncthreads();
     auto part = [&](int b, int j) { return p.parts + (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * X::kPart; };
 
-    for (int w = blockIdx.x; w < few + many * kPairs; w += join_blocks) {
+    for (int w = blockIdx.x; w < few * NT + many * kPairs; w += join_blocks) {
         const bool pair = w < many * kPairs;
-        const int4 open = pair ? sh.list[kMaxBlocks - 1 - w / kPairs] : sh.list[w - many * kPairs];
+        const int4 open = pair ? sh.list[kMaxBlocks - 1 - w / kPairs] : sh.list[(w - many * kPairs) / NT];
         const int n = open.x, hkv = open.y / p.GT, gt = open.y % p.GT, b = open.w, k = open.z - b + 1;
         const int64_t row0 = (int64_t)n * p.Hq + hkv * p.G + gt * 8 * NT;
         const int live_heads = p.G - gt * 8 * NT;
         const float ones[2] = {1.f, 1.f};
         __syncthreads();                       // the item before has been read
         if (!pair) {
-            if (tid < 8 * NT) {                // factors exp2(m - max) / sum of each part
+            const int nt = (w - many * kPairs) % NT, r0 = nt * (D / 4) + warp * kShare;
+            if (nt * 8 >= live_heads) continue;
+            float x[kFew][kShare], y[kShare], z[kShare];           // all parts on their way at once
+            load_gate<T, D, kShare>(p, row0, live_heads, r0, lane, z);
+#pragma unroll
+            for (int j = 0; j < kFew; ++j)
+#pragma unroll
+                for (int r = 0; r < kShare; ++r) x[j][r] = j < k ? part(b, j)[(r0 + r) * 32 + lane] : 0.f;
+            if (tid < 8) {                     // factors exp2(m - max) / sum of each part
                 float m[kFew], l[kFew], mx = -INFINITY, sm = 0.f;
 #pragma unroll
                 for (int j = 0; j < kFew; ++j) {
-                    m[j] = j < k ? part(b, j)[X::kRegs * 32 + tid] : -INFINITY;
-                    l[j] = j < k ? part(b, j)[X::kRegs * 32 + 8 * NT + tid] : 0.f;
+                    m[j] = j < k ? part(b, j)[X::kRegs * 32 + nt * 8 + tid] : -INFINITY;
+                    l[j] = j < k ? part(b, j)[X::kRegs * 32 + 8 * NT + nt * 8 + tid] : 0.f;
                     mx = fmaxf(mx, m[j]);
                 }
                 const float base = mx == -INFINITY ? 0.f : mx;
@@ -916,24 +924,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
 #pragma unroll
                 for (int j = 0; j < kFew; ++j) sh.few[j][tid] = m[j] * inv;
             }
-            float x[kShare], y[kShare], z[kShare];
-            load_gate<T, D, kShare>(p, row0, live_heads, warp * kShare, lane, z);
-#pragma unroll
-            for (int r = 0; r < kShare; ++r) y[r] = 0.f;
             __syncthreads();
-#pragma unroll 2
-            for (int j = 0; j < k; ++j) {
-                const float* src = part(b, j) + warp * kShare * 32 + lane;
 #pragma unroll
-                for (int r = 0; r < kShare; ++r) x[r] = src[r * 32];
+            for (int r = 0; r < kShare; ++r) {
+                y[r] = 0.f;
 #pragma unroll
-                for (int r = 0; r < kShare; ++r) {
-                    int h, ch;
-                    part_coord<T, D>(warp * kShare + r, lane, h, ch);
-                    y[r] += x[r] * sh.few[j][h];
-                }
+                for (int j = 0; j < kFew; ++j) y[r] += x[j][r] * sh.few[j][2 * (lane & 3) + (r & 1)];
             }
-            store_out<T, D, kShare>(p, row0, live_heads, warp * kShare, lane, y, z, ones);
+            store_out<T, D, kShare>(p, row0, live_heads, r0, lane, y, z, ones);
             continue;
         }
         const int r0 = w % kPairs * 2, nt = r0 / (D / 4);
