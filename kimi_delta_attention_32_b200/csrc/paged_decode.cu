@@ -746,7 +746,7 @@ paged_decode_kernel(const Params p) {
     write_empty();
 }
 
-constexpr int kJoinWarps = 8, kJoinPerSm = 4, kFew = 8;
+constexpr int kJoinWarps = 8, kJoinPerSm = 3, kFew = 8;
 
 // acc[n, h, j] += sum over the group's heads of exp2(score - max) / sum: 1024 slots of one head a
 // block, four a thread. The maximum and sum of a segment that spans blocks come from its parts, so
