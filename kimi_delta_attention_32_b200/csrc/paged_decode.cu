@@ -21,8 +21,8 @@
 // With M >= 64 rows an instruction, the tcgen05 path would be at least 7/8 padding for such G and
 // its operands would pass through tensor memory; the warp-level MMA feeds from ldmatrix directly
 // and needs a tenth of the tile's streaming time.
-//  - bf16: m16n8k16, P rounded to bf16 (each weight off by half a step, 2^-9 of it on average:
-//    below the rounding of the output itself); l sums the unrounded weights in fp32.
+//  - bf16: m16n8k16, P as the sum of two bf16 (one would add an error as large as the rounding of
+//    the output, 1.35 times it together; the second product is free beside the stream).
 //  - fp32: m16n8k8 TF32, each operand split in two (x = hi + lo, both TF32) and three products,
 //    which leaves about 2^-20 of a product at most, and 2^-22 of it on average.
 //
@@ -86,18 +86,21 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& l
     hi = (x + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) & 0xffffe000u;
 }
-// d + dl + dh += a b to fp32's accuracy: the large product and the two small cross products, each
-// into its own accumulator (or the same one).
-__device__ __forceinline__ void mma_f32(float* d, float* dl, float* dh, const uint32_t* a, uint32_t b0,
-                                        uint32_t b1) {
+// d += a b to fp32's accuracy: the two small cross products, then the large one. The tensor cores cut
+// their sums instead of rounding them; over a long cache that adds up (1.8e-6 of the output was
+// measured, 2.4e-7 this way), so a step's sum starts at zero and is added to d in fp32.
+__device__ __forceinline__ void mma_f32(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
     uint32_t ah[4], al[4], bh0, bh1, bl0, bl1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
     split_tf32(b0, bh0, bl0);
     split_tf32(b1, bh1, bl1);
-    mma_tf32(dl, al, bh0, bh1);
-    mma_tf32(dh, ah, bl0, bl1);
-    mma_tf32(d, ah, bh0, bh1);
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_tf32(t, al, bh0, bh1);
+    mma_tf32(t, ah, bl0, bl1);
+    mma_tf32(t, ah, bh0, bh1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] += t[i];
 }
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -511,17 +514,12 @@ paged_decode_kernel(const Params p) {
             }
         }
 
-        // S^T = K Q^T: rows slots, columns heads. Several accumulators shorten the chain.
-        constexpr int kAccs = kBf16 ? 2 : 3;
-        float s[NT][4], sx[kAccs - 1][NT][4];
+        // S^T = K Q^T: rows slots, columns heads. Two accumulators halve the chain.
+        float s[NT][4], s2[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                s[nt][c] = 0.f;
-#pragma unroll
-                for (int u = 0; u < kAccs - 1; ++u) sx[u][nt][c] = 0.f;
-            }
+            for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
         // (fp32's 16 or 8 steps of three products and their splits are kept a loop: unrolled, the
         // tile's code no longer fits the instruction cache)
 #pragma unroll (kBf16 ? X::kPieces / 4 : 1)
@@ -540,10 +538,10 @@ paged_decode_kernel(const Params p) {
                 }
                 if constexpr (kBf16) {
                     mma_bf16(s[nt], a0, bq[0], bq[1]);
-                    mma_bf16(sx[0][nt], a1, bq[2], bq[3]);
+                    mma_bf16(s2[nt], a1, bq[2], bq[3]);
                 } else {
-                    mma_f32(s[nt], sx[0][nt], sx[kAccs - 2][nt], a0, bq[0], bq[1]);
-                    mma_f32(s[nt], sx[0][nt], sx[kAccs - 2][nt], a1, bq[2], bq[3]);
+                    mma_f32(s[nt], a0, bq[0], bq[1]);
+                    mma_f32(s2[nt], a1, bq[2], bq[3]);
                 }
             }
         }
@@ -553,9 +551,7 @@ paged_decode_kernel(const Params p) {
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-#pragma unroll
-                for (int u = kAccs - 2; u > 0; --u) sx[u - 1][nt][c] += sx[u][nt][c];
-                s[nt][c] = (c < 2 ? ok0 : ok1) ? (s[nt][c] + sx[0][nt][c]) * p.scale_log2 : -INFINITY;
+                s[nt][c] = (c < 2 ? ok0 : ok1) ? (s[nt][c] + s2[nt][c]) * p.scale_log2 : -INFINITY;
                 above |= s[nt][c] > m[nt][c & 1] + kSlack;
             }
             if (scores != nullptr) {
@@ -605,13 +601,17 @@ paged_decode_kernel(const Params p) {
         if (++k_unit == U) k_unit = 0;
         const uint32_t vd = smem_u32(ring) + v_unit * X::kUnit;
         if constexpr (kBf16) {
-            uint32_t pb[NT][2];
+            uint32_t ph[NT][2], pl[NT][2];                         // P = hi + lo, both bf16
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const __nv_bfloat162 w = __floats2bfloat162_rn(s[nt][2 * e], s[nt][2 * e + 1]);
-                    pb[nt][e] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+                    const float x = s[nt][2 * e], y = s[nt][2 * e + 1];
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(x, y);
+                    const float2 f = __bfloat1622float2(hi);
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(x - f.x, y - f.y);
+                    ph[nt][e] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
+                    pl[nt][e] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
                 }
             const int vr = (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
@@ -619,7 +619,10 @@ paged_decode_kernel(const Params p) {
                 uint32_t a[4];
                 ldsm4_t(vd + vr * X::kRowBytes + (((2 * mt + ((lane >> 3) & 1)) ^ (vr & 7)) << 4), a);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_bf16(out[nt][mt], a, pb[nt][0], pb[nt][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_bf16(out[nt][mt], a, pl[nt][0], pl[nt][1]);
+                    mma_bf16(out[nt][mt], a, ph[nt][0], ph[nt][1]);
+                }
             }
         } else {
 #pragma unroll 1
@@ -647,9 +650,8 @@ paged_decode_kernel(const Params p) {
                     const uint32_t a0[4] = {x.x, x.y, y.x, y.y}, a1[4] = {x.z, x.w, y.z, y.w};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_f32(out[nt][2 * pc], out[nt][2 * pc], out[nt][2 * pc], a0, pb[nt][0], pb[nt][1]);
-                        mma_f32(out[nt][2 * pc + 1], out[nt][2 * pc + 1], out[nt][2 * pc + 1], a1,
-                                pb[nt][0], pb[nt][1]);
+                        mma_f32(out[nt][2 * pc], a0, pb[nt][0], pb[nt][1]);
+                        mma_f32(out[nt][2 * pc + 1], a1, pb[nt][0], pb[nt][1]);
                     }
                 }
             }

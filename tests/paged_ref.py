@@ -34,9 +34,9 @@ def append(k_cache, v_cache, table, lens, k, v, cu, seen=None, acc=None, pos=Non
 
 
 def decode(q, k_cache, v_cache, table, lens, scale, z=None, skip=None):
-    """(o, weights per sequence [Hkv, len], elementwise bound of o in its type's half steps, bound
-    of the weights). skip(n, page) -> True for slots of pages to leave out. fp64 numpy in and out;
-    the bound's type part is left to the caller as (abs_sum, o, rel)."""
+    """(o, weights per sequence [Hkv, len], sum_j w_j |V_j|, relative error of the weights and
+    sums in the device's fp32). skip(page numbers) -> True for slots to leave out. fp64 numpy in and
+    out."""
     N, Hq, d = q.shape
     H = k_cache.shape[2]
     G, page = Hq // H, k_cache.shape[1]
@@ -75,9 +75,9 @@ def decode(q, k_cache, v_cache, table, lens, scale, z=None, skip=None):
 
 
 def decode_bound(io, o, mag, rel):
-    """Elementwise bound: the weights rounded to the io type before their product with V, and the
-    output rounded to it (half a step each), beside the fp32 part."""
-    return (HALF[io] * (1 + 2.0 ** -7) + rel) * mag + HALF[io] * np.abs(o) + 1e-30
+    """Elementwise bound: the weights as the sum of two bf16 (2^-16; fp32 splits lie below that),
+    the output rounded to the io type (half a step), beside the fp32 part."""
+    return (2.0 ** -16 + rel) * mag + HALF[io] * (np.abs(o) + (2.0 ** -16 + rel) * mag) + 1e-30
 
 
 def evict(k_cache, v_cache, table, lens, keep, acc, pos, seen, n_first, n_recent):
