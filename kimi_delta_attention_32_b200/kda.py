@@ -499,6 +499,17 @@ def _call_on(dev, stream, fn, *args):
     return fn(*args, _stream(stream))
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream of the call: freed, its memory goes to that stream's
+    later work only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def cache_append(k, v, k_cache, v_cache, block_table, seqlens, positions=None, acc=None, pos=None,
                  cu_seqlens=None, cu_host=None, stream=None):
     """Writes new tokens into the paged cache: token i of sequence n to slot seqlens[n] + i.
@@ -573,7 +584,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seqlens, scale=1.0, z=None, a
     q_p = _need("q", q, dtype, shape, dev)
     z_p = _may("z", z, dtype, shape, dev)
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(shape, dtype, q.device, stream)
     o_p = _need("o", o, dtype, shape, dev)
     slots = acc.shape[-1] if acc is not None else 0
     acc_p = _may("acc", acc, torch.float32, (N, H, slots), dev)
@@ -583,9 +594,11 @@ def paged_decode(q, k_cache, v_cache, block_table, seqlens, scale=1.0, z=None, a
         max_len = cache[8] * page_size
         if acc is not None:
             max_len = min(max_len, slots)
+    if not max_len < 1 << 31:
+        raise ValueError("max_len is int32")
     if workspace is None and dev >= 0:
-        workspace = torch.empty(paged_decode_workspace_size(N, Hq, H, d, max_len, acc is not None),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _empty(paged_decode_workspace_size(N, Hq, H, d, max_len, acc is not None),
+                           torch.uint8, q.device, stream)
     ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (None, 0)
     st = _call_on(dev, stream, lib.kda_paged_decode, q_p, *cache, z_p, scale, acc_p, slots, o_p, N,
                   Hq, H, d, max_len, io, ws, ws_bytes)
@@ -619,15 +632,17 @@ def cache_evict(k_cache, v_cache, block_table, seqlens, keep, acc, pos, position
     ao_p = acc_p if acc_out is None else _need("acc_out", acc_out, torch.float32, shape, dev)
     po_p = pos_p if pos_out is None else _need("pos_out", pos_out, torch.int32, shape, dev)
     if seqlens_out is None:
-        seqlens_out = torch.empty_like(seqlens)
+        seqlens_out = _empty((N,), torch.int32, seqlens.device, stream)
     out_p = _need("seqlens_out", seqlens_out, torch.int32, (N,), dev)
     if N == 0:
         return seqlens_out
     if max_len is None:
         max_len = min(cache[8] * page_size, slots)
+    if not max(keep, n_first, n_recent, max_len) < 1 << 31:      # ctypes would cut them
+        raise ValueError("keep, n_first, n_recent and max_len are int32")
     if workspace is None and dev >= 0:
-        workspace = torch.empty(cache_evict_workspace_size(N, H, max_len, keep), dtype=torch.uint8,
-                                device=seqlens.device)
+        workspace = _empty(cache_evict_workspace_size(N, H, max_len, keep), torch.uint8,
+                           seqlens.device, stream)
     ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (None, 0)
     st = _call_on(dev, stream, lib.kda_cache_evict, *cache, seen_p, keep, n_first, n_recent, acc_p,
                   pos_p, ao_p, po_p, slots, out_p, N, H, d, max_len, io, ws, ws_bytes)

@@ -297,6 +297,57 @@ def test_two_streams_at_once():
         assert torch.equal(a, b)
 
 
+def test_default_workspace_on_another_stream():
+    """What a call allocates on its own belongs to the call's stream: work on the current stream,
+    which soon takes over the freed memory, does not write into it."""
+    c = Paged("bf16", [9000, 4000], 2, 128, 16, seed=21)
+    q = c.rand(2, 8, 128)
+    want = kda.paged_decode(q, *c.args, scale=0.1)
+    size = kda.paged_decode_workspace_size(2, 8, 2, 128, c.max_pages * 16)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = []
+    for i in range(20):
+        outs.append(kda.paged_decode(q, *c.args, scale=0.1, stream=s if i % 2 else s.cuda_stream))
+        torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls with one workspace, replayed in turns."""
+    cs = [Paged("bf16", [3000, 70], 2, 128, 16, seed=30), Paged("bf16", [500, 2000], 2, 128, 16, seed=31)]
+    qs = [c.rand(2, 8, 128) for c in cs]
+    want = [kda.paged_decode(q, *c.args, scale=0.1) for c, q in zip(cs, qs)]
+    slots = max(c.max_pages for c in cs) * 16
+    ws = torch.empty(kda.paged_decode_workspace_size(2, 8, 2, 128, slots), dtype=torch.uint8, device=DEV)
+    outs = [torch.zeros_like(q) for q in qs]
+    graphs = []
+    for c, q, o in zip(cs, qs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kda.paged_decode(q, *c.args, scale=0.1, workspace=ws, o=o)
+        graphs.append(g)
+    for _ in range(5):
+        for g, o, w in zip(graphs, outs, want):
+            o.zero_()
+            g.replay()
+            assert torch.equal(o, w)
+
+
+def test_keys_that_are_the_values():
+    """One tensor as both caches, and shared pages: reading needs no page to be a sequence's own."""
+    c = Paged("bf16", [100, 100, 40], 2, 64, 16, seed=32)
+    c.v = c.k
+    c.table[1] = c.table[0]
+    c.table[2, :3] = c.table[0, :3]
+    c.tab = c.table.to(DEV)
+    q = c.rand(3, 4, 64)
+    acc = c.acc.clone()
+    check_decode(c, q, kda.paged_decode(q, *c.args, scale=0.2, acc=acc), 0.2, None, acc, c.acc)
+
+
 # ---------------------------------------------------------------- append
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])

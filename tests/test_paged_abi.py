@@ -233,5 +233,9 @@ def test_binding_refuses():
         kda.cache_evict(keep=8, acc=acc, pos=pos, workspace=ws, **t)
     with pytest.raises(ValueError, match="shape"):
         kda.cache_evict(keep=8, acc=acc, pos=pos[:, :, :32], workspace=ws, **t)
+    with pytest.raises(ValueError, match="int32"):
+        kda.cache_evict(keep=(1 << 32) + 8, acc=acc, pos=pos, workspace=ws, **t)
+    with pytest.raises(ValueError, match="int32"):
+        dec(max_len=1 << 32)
     with pytest.raises(TypeError, match="required"):
         kda.cache_evict(keep=8, acc=acc, pos=None, workspace=ws, **t)
