@@ -145,6 +145,7 @@ struct Params {
     int N, Hq, H, G, GT;             // GT: head tiles of a group
     int max_len;
     int most_blocks;
+    int whole;                       // > 0: a block a segment, of at most so many tiles; no joins
     int* meta;                       // [blocks][4]: n, head * GT + gt, last block of a segment to join
     float* parts;                    // [2 blocks][kPart]: a block's first and last segments' parts
     // for acc: scores (log2 units) [tile][GS][kTile]; {max, 1 / sum} [N, Hq] of the segments inside
@@ -213,10 +214,31 @@ paged_decode_kernel(const Params p) {
     const int heads = p.H * p.GT;                                  // segments of a sequence
     const T* q = static_cast<const T*>(p.q);
 
-    // ---- the block's range of tiles. Up to 32 sequences every warp scans their tiles on its own;
-    // more are summed by groups first, the warps sharing them, in the ring that is still empty.
+    // ---- the block's tiles: `count` of them from tile t0 of all on, the first at `cur`
     auto len_of = [&](int n) { return checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err); };
     auto tiles_of = [&](int len) { return (len + kTile - 1) / kTile; };
+    struct Cursor { int n, hkv, gt, tile, len, tiles; };
+    Cursor cur;
+    const int b = blockIdx.x;
+    int64_t t0, all_tiles = 0;
+    int count, C = 0;
+    if (p.whole > 0) {
+        cur.n = b / heads;
+        cur.hkv = (b - cur.n * heads) / p.GT;
+        cur.gt = b - cur.n * heads - cur.hkv * p.GT;
+        cur.tile = 0;
+        cur.len = len_of(cur.n);
+        cur.tiles = count = tiles_of(cur.len);
+        t0 = (int64_t)b * p.whole;
+        if (count == 0) {
+            const int g0 = cur.gt * 8 * NT, end = min(8 * NT, p.G - g0) * D;
+            T* o = static_cast<T*>(p.o) + ((int64_t)cur.n * p.Hq + cur.hkv * p.G + g0) * D;
+            for (int e = tid; e < end; e += kThreads) o[e] = from_f32<T>(0.f);
+            return;
+        }
+    } else {
+    // Up to 32 sequences every warp scans their tiles on its own; more are summed by groups first,
+    // the warps sharing them, in the ring that is still empty.
     auto tiles_at = [&](int n, int end) { return n < end ? tiles_of(len_of(n)) : 0; };
     auto warp_scan = [&](int x) {
 #pragma unroll
@@ -248,20 +270,15 @@ paged_decode_kernel(const Params p) {
         mine = tiles_at(lane, p.N);
     }
     const int incl = warp_scan(mine);
-    const int64_t work = (int64_t)__shfl_sync(0xffffffffu, incl, 31) * heads;
-    const int C = split_blocks(work, p.most_blocks), b = blockIdx.x;
-    // sequences of length 0 have no tiles: their outputs are written here
-    auto write_empty = [&]() {
-        for (int n = b; n < p.N; n += gridDim.x)
-            if (len_of(n) == 0)
-                for (int e = tid; e < p.Hq * D; e += kThreads)
-                    static_cast<T*>(p.o)[(int64_t)n * p.Hq * D + e] = from_f32<T>(0.f);
-    };
+    const int64_t work = all_tiles = (int64_t)__shfl_sync(0xffffffffu, incl, 31) * heads;
+    C = split_blocks(work, p.most_blocks);
     if (tid == 0) p.meta[4 * b + 2] = -1;
-    if (b >= C) {
-        write_empty();
-        return;
-    }
+    // sequences of length 0 have no tiles: their outputs are written here
+    for (int n = b; n < p.N; n += gridDim.x)
+        if (len_of(n) == 0)
+            for (int e = tid; e < p.Hq * D; e += kThreads)
+                static_cast<T*>(p.o)[(int64_t)n * p.Hq * D + e] = from_f32<T>(0.f);
+    if (b >= C) return;
     if (p.tiles_before != nullptr && warp == 0) {
         if (b == 0 && lane == 31) p.tiles_before[p.N] = incl;
         if (!grouped) {
@@ -279,8 +296,8 @@ paged_decode_kernel(const Params p) {
             }
         }
     }
-    const int64_t t0 = split_begin(work, C, b);
-    const int count = (int)(split_begin(work, C, b + 1) - t0);
+    t0 = split_begin(work, C, b);
+    count = (int)(split_begin(work, C, b + 1) - t0);
     const int target = (int)split_div(t0, heads);      // tiles of earlier sequences <= target
     const int owner = __ffs(__ballot_sync(0xffffffffu, mine > 0 && target < incl)) - 1;
     int first_n = owner, first_before = __shfl_sync(0xffffffffu, incl - mine, owner);
@@ -302,8 +319,17 @@ paged_decode_kernel(const Params p) {
         __syncthreads();                               // the sums have been read: the ring may fill
     }
 
-    // ---- a position in the order of tiles: sequence, key-value head, head tile, tile
-    struct Cursor { int n, hkv, gt, tile, len, tiles; };
+    cur.n = first_n;
+    cur.len = len_of(cur.n);
+    cur.tiles = tiles_of(cur.len);
+    const int64_t in_seq = t0 - (int64_t)first_before * heads;
+    const int head = (int)split_div(in_seq, cur.tiles);
+    cur.tile = (int)(in_seq - (int64_t)head * cur.tiles);
+    cur.hkv = head / p.GT;
+    cur.gt = head % p.GT;
+    }
+
+    // on to the next segment: head tile, key-value head, sequence
     auto next_segment = [&](Cursor& u) {
         u.tile = 0;
         if (++u.gt < p.GT) return;
@@ -316,17 +342,6 @@ paged_decode_kernel(const Params p) {
         } while (u.len == 0);
         u.tiles = tiles_of(u.len);
     };
-    Cursor cur;
-    cur.n = first_n;
-    cur.len = len_of(cur.n);
-    cur.tiles = tiles_of(cur.len);
-    {
-        const int64_t in_seq = t0 - (int64_t)first_before * heads;
-        const int head = (int)split_div(in_seq, cur.tiles);
-        cur.tile = (int)(in_seq - (int64_t)head * cur.tiles);
-        cur.hkv = head / p.GT;
-        cur.gt = head % p.GT;
-    }
 
     // ---- page numbers: with kRuns one for the warp's 16 slots of a tile, else lanes l and l + 16
     // hold slot l's. That of the tile behind the next is on its way while the next one's is used; the
@@ -733,7 +748,7 @@ paged_decode_kernel(const Params p) {
                 const int64_t last = t0 + i + (cur.tiles - 1 - cur.tile);
                 p.meta[4 * b] = cur.n;
                 p.meta[4 * b + 1] = cur.hkv * p.GT + cur.gt;
-                p.meta[4 * b + 2] = split_block_of(work, C, last);
+                p.meta[4 * b + 2] = split_block_of(all_tiles, C, last);
             }
             reset();
             if (++at_q == NQ) at_q = 0;
@@ -745,7 +760,6 @@ paged_decode_kernel(const Params p) {
     }
     cp_wait<0>();
     grid_release();
-    write_empty();
 }
 
 constexpr int kJoinWarps = 8, kJoinPerSm = 3, kFew = 8;
@@ -764,17 +778,20 @@ __device__ __forceinline__ void gather_weights(const Params& p, int block, int b
         const int64_t nh = w / chunks, n = nh / p.H;
         const int j = (int)(w % chunks) * kWeightSlots + tid * 4, h = (int)(nh % p.H);
         const int len = checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err);
-        const int64_t before = p.tiles_before[n], work = (int64_t)p.tiles_before[p.N] * p.H * p.GT;
+        const int64_t before = p.whole > 0 ? 0 : p.tiles_before[n];
+        const int64_t work = p.whole > 0 ? 1 : (int64_t)p.tiles_before[p.N] * p.H * p.GT;
         if ((int)(w % chunks) * kWeightSlots >= len) continue;     // the whole block agrees
         float* acc = p.acc + nh * p.slots + j;
         float old[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < 4; ++u) old[u] = j + u < len ? acc[u] : 0.f;
-        const int tiles = (len + X::kTile - 1) / X::kTile, C = split_blocks(work, p.most_blocks);
-        const int64_t seg = (before * p.H + (int64_t)h * tiles) * p.GT;        // the head's first tile
+        const int tiles = p.whole > 0 ? p.whole : (len + X::kTile - 1) / X::kTile;
+        const int C = split_blocks(work, p.most_blocks);
+        const int64_t seg = (p.whole > 0 ? nh * tiles : before * p.H + (int64_t)h * tiles) * p.GT;   // the head's first tile
         for (int gt = 0; gt < p.GT; ++gt) {
             const int64_t t0 = seg + (int64_t)gt * tiles;
-            const int b0 = split_block_of(work, C, t0), k = split_block_of(work, C, t0 + tiles - 1) - b0 + 1;
+            const int b0 = p.whole > 0 ? 0 : split_block_of(work, C, t0);
+            const int k = p.whole > 0 ? 1 : split_block_of(work, C, t0 + tiles - 1) - b0 + 1;
             const int heads = min(8 * NT, p.G - gt * 8 * NT);
             // four heads' scores are on their way while the statistics are formed
             const float* s = p.scores + (t0 + j / X::kTile) * p.GS * X::kTile + j % X::kTile;
@@ -1043,14 +1060,24 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     auto kernel = runs ? paged_decode_kernel<T, D, NT, true> : paged_decode_kernel<T, D, NT, false>;
     cudaError_t e = allow_smem(kernel, X::kSmem, allowed[runs]);
     if (e != cudaSuccess) return e;
-    kernel<<<p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
+    // Short segments, no more than blocks, are a block each: the scan of the lengths and the joins
+    // cost about five tiles' time, more than dividing gains while t tiles in sequence are no more
+    // than five above the t S / C of a divided block. (8 heads of one sequence: 200 slots 7.8 us
+    // whole, 8.4 divided, 512 slots 10.9 and 8.5; 128 segments: 512 slots 11.0 and 13.0, 1024 slots
+    // 17.4 and 16.3.) max_len may be far above the lengths, whose balance the division keeps: 16 at
+    // most.
+    const int64_t segments = (int64_t)a.N * a.H * p.GT, blocks = p.most_blocks;
+    const int64_t t = (a.max_len + X::kTile - 1) / X::kTile;
+    p.whole = segments <= blocks && t <= 16 && t * (blocks - segments) <= 5 * blocks ? (int)t : 0;
+    kernel<<<p.whole > 0 ? (unsigned)segments : p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (p.whole > 0 && a.acc == nullptr) return cudaSuccess;
     int join_blocks = sms * kJoinPerSm;
     int64_t weight_blocks = 0;
     if (a.acc != nullptr) {
         weight_blocks = (int64_t)a.N * a.H * ((a.max_len + kWeightSlots - 1) / kWeightSlots);
         if (weight_blocks > sms * kJoinPerSm) weight_blocks = sms * kJoinPerSm;
-        join_blocks /= 2;
+        join_blocks = p.whole > 0 ? 0 : join_blocks / 2;
     }
     return launch_after(paged_join_kernel<T, D, NT>, dim3(join_blocks + (unsigned)weight_blocks),
                         kJoinWarps * 32, stream, p, join_blocks);
