@@ -529,12 +529,14 @@ paged_decode_kernel(const Params p) {
             }
         }
 
-        // S^T = K Q^T: rows slots, columns heads. Two accumulators halve the chain.
-        float s[NT][4], s2[NT][4];
+        // S^T = K Q^T: rows slots, columns heads. Two accumulators halve the chain; four tiles of
+        // heads are chains enough, and need the registers.
+        constexpr bool kTwo = NT < 4;
+        float s[NT][4], s2[kTwo ? NT : 1][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
+            for (int c = 0; c < 4; ++c) s[nt][c] = s2[kTwo ? nt : 0][c] = 0.f;
         // (fp32's 16 or 8 steps of three products and their splits are kept a loop: unrolled, the
         // tile's code no longer fits the instruction cache)
 #pragma unroll (kBf16 ? X::kPieces / 4 : 1)
@@ -553,10 +555,10 @@ paged_decode_kernel(const Params p) {
                 }
                 if constexpr (kBf16) {
                     mma_bf16(s[nt], a0, bq[0], bq[1]);
-                    mma_bf16(s2[nt], a1, bq[2], bq[3]);
+                    mma_bf16(kTwo ? s2[kTwo ? nt : 0] : s[nt], a1, bq[2], bq[3]);
                 } else {
                     mma_f32(s[nt], a0, bq[0], bq[1]);
-                    mma_f32(s2[nt], a1, bq[2], bq[3]);
+                    mma_f32(kTwo ? s2[kTwo ? nt : 0] : s[nt], a1, bq[2], bq[3]);
                 }
             }
         }
@@ -566,7 +568,7 @@ paged_decode_kernel(const Params p) {
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                s[nt][c] = (c < 2 ? ok0 : ok1) ? (s[nt][c] + s2[nt][c]) * p.scale_log2 : -INFINITY;
+                s[nt][c] = (c < 2 ? ok0 : ok1) ? (s[nt][c] + s2[kTwo ? nt : 0][c]) * p.scale_log2 : -INFINITY;
                 above |= s[nt][c] > m[nt][c & 1] + kSlack;
             }
             if (scores != nullptr) {
