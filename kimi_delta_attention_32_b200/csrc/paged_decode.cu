@@ -777,12 +777,13 @@ __device__ __forceinline__ void gather_weights(const Params& p, int block, int b
     const int chunks = (p.max_len + kWeightSlots - 1) / kWeightSlots;
     const int64_t all = (int64_t)p.N * p.H * chunks;
     for (int64_t w = block; w < all; w += blocks) {
-        const int64_t nh = w / chunks, n = nh / p.H;
-        const int j = (int)(w % chunks) * kWeightSlots + tid * 4, h = (int)(nh % p.H);
+        const int64_t nh = split_div(w, chunks), n = (uint32_t)nh / (uint32_t)p.H;     // nh < 2^31
+        const int chunk = (int)(w - nh * chunks), h = (int)(nh - n * p.H);
+        const int j = chunk * kWeightSlots + tid * 4;
         const int len = checked_len(__ldg(p.seqlens + n), p.max_len, p.c.err);
         const int64_t before = p.whole > 0 ? 0 : p.tiles_before[n];
         const int64_t work = p.whole > 0 ? 1 : (int64_t)p.tiles_before[p.N] * p.H * p.GT;
-        if ((int)(w % chunks) * kWeightSlots >= len) continue;     // the whole block agrees
+        if (chunk * kWeightSlots >= len) continue;                 // the whole block agrees
         float* acc = p.acc + nh * p.slots + j;
         float old[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
