@@ -416,9 +416,12 @@ kda_status kda_fused_recurrent_step(const void* q_raw, const void* k_raw, const 
  *  Lengths and page numbers are checked on the device: a length outside its range is clamped, and
  *  a slot whose page number is not in [0, num_pages) is left out (not attended to, not written);
  *  either sets the device error word, and kda_last_device_error then returns KDA_ERR_INDEX.
+ *  Make the first of these calls on a device before any stream capture (they look up the error word
+ *  and set kernel attributes once).
  *  Not checked: that no two slots share memory (a page twice in the tables of what one call
  *  writes), and finite inputs.
- *  Supported: d in {64, 128}, io F32 or BF16, any page_size, max_pages * page_size <= 2^30.
+ *  Supported: d in {64, 128}, io F32 or BF16, any page_size, max_pages * page_size <= 2^30,
+ *  N * max_len <= 2^36.
  */
 
 /*

@@ -19,10 +19,11 @@
 // sum and output in registers, so warps meet only at a segment's end. The slots are the M side of
 // the products and the queries the N side (padded to 8, not 16): S^T = K Q^T and O^T = V^T P^T.
 // With M >= 64 rows an instruction, the tcgen05 path would be at least 7/8 padding for such G and
-// its operands would pass through tensor memory; the warp-level MMA feeds from ldmatrix directly
-// and needs a tenth of the tile's streaming time.
+// its operands would pass through tensor memory; the warp-level MMA feeds from ldmatrix directly,
+// and with 4 queries a head its pipe is busy 14% of the time (32 sequences of 4000 slots).
 //  - bf16: m16n8k16, P as the sum of two bf16 (one would add an error as large as the rounding of
-//    the output, 1.35 times it together; the second product is free beside the stream).
+//    the output, 1.35 times it together; the second product costs about 1% of the time for G <= 8
+//    and a tenth for G >= 16).
 //  - fp32: m16n8k8 TF32, each operand split in two (x = hi + lo, both TF32) and three products,
 //    which leaves about 2^-20 of a product at most, and 2^-22 of it on average.
 //
@@ -31,6 +32,10 @@
 // first tile and its end. 16-byte piece c of row r lies at piece c ^ (r % 8): ldmatrix reads eight
 // rows without a bank conflict. Page numbers are read two tiles before their rows are.
 // Rows behind the end or with a bad page number are filled with zeros and masked.
+//
+// Measured on one B200, whole calls: 64 sequences of 128 to 16384 tokens, 32 query and 8 key-value
+// heads of 128, bf16, with the gate, 352 to 361 us, 97 to 100% of the 6459 GB/s of a copy; 262144
+// tokens, 8 and 2 heads, 54 us, of which 9 are the join; fp32, 32 sequences of 4096, 96 to 100%.
 #include "decode_split.h"
 #include "paged.cuh"
 
@@ -113,7 +118,7 @@ __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)
 //  - two blocks of 4 warps an SM, three where a row is 128 bytes and the registers allow: a block's
 //    join of its warps then overlaps the others' streams. fp32 rows of 512 bytes leave room for one
 //    block, of 8 warps with three units each;
-//  - 96 to 160 KB of rows an SM are in flight beside what is being read;
+//  - 128 to 168 KB of rows an SM are in flight beside what is being read;
 //  - every tile in flight, and the current one, may begin a segment: room for NQ segments' queries.
 template <typename T, int D, int NT>
 struct Shape {
@@ -790,7 +795,8 @@ __device__ __forceinline__ void gather_weights(const Params& p, int block, int b
         for (int u = 0; u < 4; ++u) old[u] = j + u < len ? acc[u] : 0.f;
         const int tiles = p.whole > 0 ? p.whole : (len + X::kTile - 1) / X::kTile;
         const int C = split_blocks(work, p.most_blocks);
-        const int64_t seg = (p.whole > 0 ? nh * tiles : before * p.H + (int64_t)h * tiles) * p.GT;   // the head's first tile
+        // the head's first tile
+        const int64_t seg = (p.whole > 0 ? nh * tiles : before * p.H + (int64_t)h * tiles) * p.GT;
         for (int gt = 0; gt < p.GT; ++gt) {
             const int64_t t0 = seg + (int64_t)gt * tiles;
             const int b0 = p.whole > 0 ? 0 : split_block_of(work, C, t0);
@@ -977,9 +983,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) paged_join_kernel
                 sm += f * sh.l[j][warp];
             }
             sm = warp_sum(sm);
-            if (lane == 0) {
-                sh.sum[warp] = sm > 0.f ? 1.f / sm : 0.f;
-            }
+            if (lane == 0) sh.sum[warp] = sm > 0.f ? 1.f / sm : 0.f;
         }
         __syncthreads();
         float y0 = 0.f, y1 = 0.f;

@@ -114,8 +114,17 @@ EDGE = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 200]
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G,H", [(1, 3), (4, 2), (8, 2), (12, 1), (32, 1)])
-def test_decode_edge_lengths(io, d, G, H):
-    decode_case(io, EDGE, G * H, H, d, 16, gate=True, acc=True, seed=G)
+@pytest.mark.parametrize("more", [[], [1500]], ids=["whole", "divided"])
+def test_decode_edge_lengths(io, d, G, H, more):
+    """The short ones alone are a block each; with a long one among them the tiles are divided."""
+    decode_case(io, EDGE + more, G * H, H, d, 16, gate=True, acc=True, seed=G)
+
+
+@pytest.mark.parametrize("lens,Hq,H", [([2000, 100], 71, 1), ([700, 0, 1300], 48, 2), ([1100] * 5, 20, 1)])
+def test_decode_divided_groups(lens, Hq, H):
+    """Groups of several head tiles, whose segments the division cuts."""
+    decode_case("bf16", lens, Hq, H, 128, 24, gate=True, acc=True, seed=Hq)
+    decode_case("f32", lens, Hq, H, 64, 32, acc=True, seed=Hq)
 
 
 @pytest.mark.parametrize("G", [2, 3, 5, 7, 9, 16, 17, 24, 33, 71])
