@@ -511,6 +511,21 @@ kda_status kda_cache_evict(void* k_cache, void* v_cache, int64_t page_stride, in
                            kda_io_dtype io, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * kda_paged_call -- kda_cache_append, kda_paged_decode or kda_cache_evict (which) with its
+ * arguments as 64-bit words in the order of its parameters: pointers and integers as they are,
+ * scale as a double. For callers to whom each argument costs, such as Python's ctypes (25 of them
+ * 3 us, one 0.5 us). n_words: the number of the function's parameters. KDA_ERR_INVALID_ARG for
+ * another number, and for a word that an int parameter cannot hold.
+ */
+typedef enum {
+    KDA_CALL_CACHE_APPEND = 0,
+    KDA_CALL_PAGED_DECODE = 1,
+    KDA_CALL_CACHE_EVICT = 2
+} kda_paged_function;
+
+kda_status kda_paged_call(kda_paged_function which, const void* words, int n_words);
+
+/*
  * kda_set_wait_limit -- bound, in SM clock cycles, of every device-side wait of the prefill
  * kernels launched after this call on any device (0 restores the default of ~2 s). A wait that
  * runs out sets the device error word (KDA_ERR_TIMEOUT from kda_last_device_error) and the

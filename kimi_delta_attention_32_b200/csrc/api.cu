@@ -7,8 +7,12 @@
 
 #include <stdint.h>
 
+#include <string.h>
+
 #include <atomic>
 #include <initializer_list>
+#include <type_traits>
+#include <utility>
 
 #define KDA_API extern "C" __attribute__((visibility("default")))
 
@@ -115,6 +119,36 @@ int auto_split(int64_t longest, int64_t T_tot, int H, int64_t units, int cluster
         }
     }
     return 10 * best < 9 * unsplit ? best_p : 1;
+}
+
+// One argument from its 64-bit word: pointers, 64-bit integers, ints and enums, floats from doubles.
+template <typename A>
+bool word_fits(int64_t w) {
+    return std::is_pointer_v<A> || std::is_floating_point_v<A> || sizeof(A) == 8 || w == (int32_t)w;
+}
+template <typename A>
+A from_word(int64_t w) {
+    if constexpr (std::is_pointer_v<A>) {
+        return reinterpret_cast<A>(w);
+    } else if constexpr (std::is_floating_point_v<A>) {
+        double x;
+        memcpy(&x, &w, sizeof(x));
+        return static_cast<A>(x);
+    } else {
+        return static_cast<A>(w);
+    }
+}
+template <typename... A, size_t... I>
+kda_status call_with(kda_status (*fn)(A...), const int64_t* w, std::index_sequence<I...>) {
+    if (!(word_fits<A>(w[I]) && ...)) return KDA_ERR_INVALID_ARG;
+    return fn(from_word<A>(w[I])...);
+}
+template <typename... A>
+kda_status call_with_words(kda_status (*fn)(A...), const void* words, int n_words) {
+    if (n_words != (int)sizeof...(A)) return KDA_ERR_INVALID_ARG;
+    int64_t w[sizeof...(A)];
+    memcpy(w, words, sizeof(w));
+    return call_with(fn, w, std::index_sequence_for<A...>());
 }
 
 // The arguments that the calls on the paged cache share.
@@ -713,6 +747,16 @@ KDA_API kda_status kda_cache_evict(void* k_cache, void* v_cache, int64_t page_st
     a.io = io == KDA_IO_BF16 ? kda::Io::BF16 : kda::Io::F32;
     a.workspace = workspace;
     return from_cuda(kda::launch_cache_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
+KDA_API kda_status kda_paged_call(kda_paged_function which, const void* words, int n_words) {
+    if (words == nullptr) return KDA_ERR_INVALID_ARG;
+    switch (which) {
+        case KDA_CALL_CACHE_APPEND: return call_with_words(kda_cache_append, words, n_words);
+        case KDA_CALL_PAGED_DECODE: return call_with_words(kda_paged_decode, words, n_words);
+        case KDA_CALL_CACHE_EVICT: return call_with_words(kda_cache_evict, words, n_words);
+    }
+    return KDA_ERR_INVALID_ARG;
 }
 
 KDA_API kda_status kda_set_wait_limit(int64_t cycles) {

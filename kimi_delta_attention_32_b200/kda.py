@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -26,7 +27,8 @@ EXPORTED = ("kda_status_string", "kda_version", "kda_conv_fwd", "kda_chunk_fwd_w
             "kda_last_device_error", "kda_chunk_states", "kda_state_scan",
             "kda_chunk_fwd_split_workspace_size", "kda_chunk_fwd_split", "kda_output_correct",
             "kda_chunk_fwd_split_plan", "kda_cache_append", "kda_paged_decode_workspace_size",
-            "kda_paged_decode", "kda_cache_evict_workspace_size", "kda_cache_evict")
+            "kda_paged_decode", "kda_cache_evict_workspace_size", "kda_cache_evict",
+            "kda_paged_call")
 
 _lock = threading.Lock()
 _lib = None
@@ -119,6 +121,8 @@ def load_library(path: str = LIB_PATH):
                                         ci, fp, i32p, fp, i32p, ci, i32p, ci, ci, ci, ci, ci, vp, cs,
                                         vp]
         lib.kda_cache_evict.restype = ci
+        lib.kda_paged_call.argtypes = [ci, ctypes.c_char_p, ci]
+        lib.kda_paged_call.restype = ci
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -433,7 +437,14 @@ def fused_recurrent_step(q_raw, k_raw, v_raw, g_raw, beta_raw, w_q, w_k, w_v, co
 
 # The paged cache's calls run once a layer and decoded token, on small inputs: their checks pass
 # good arguments with few operations and leave the reasons of bad ones to _refuse. The callers keep
-# their tensors' names bound to the end: an address alone does not keep its memory.
+# their tensors' names bound to the end: an address alone does not keep its memory. The arguments go
+# to the library as words in one packed object: ctypes takes 3 us to convert 25 of them.
+
+# kda_paged_function, and the words of its parameters
+_APPEND = 0, struct.Struct("=25q").pack
+_DECODE = 1, struct.Struct("=12qd12q").pack
+_EVICT = 2, struct.Struct("=28q").pack
+
 
 def _refuse(name, t, dtype, shape, device):
     if t is None:
@@ -456,7 +467,7 @@ def _need(name, t, dtype, shape, device):
 
 
 def _may(name, t, dtype, shape, device):
-    return None if t is None else _need(name, t, dtype, shape, device)
+    return 0 if t is None else _need(name, t, dtype, shape, device)
 
 
 _IO = {torch.bfloat16: KDA_IO_BF16, torch.float32: KDA_IO_F32}
@@ -487,16 +498,16 @@ def _paged(k_cache, v_cache, block_table, seqlens):
     return args, N, page_size, H, d, dtype, io, dev
 
 
-def _call_on(dev, stream, fn, *args):
-    """fn(*args, stream) with the tensors' device current."""
+def _call_on(dev, stream, function, *args):
+    """function(*args, stream) with the tensors' device current."""
     if dev < 0:
         raise ValueError("the cache must be a CUDA tensor")
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return _call_on(dev, stream, fn, *args)
-    if stream is None:
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    return fn(*args, _stream(stream))
+            return _call_on(dev, stream, function, *args)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream).value or 0
+    which, pack = function
+    return (_lib or load_library()).kda_paged_call(which, pack(*args, raw), len(args) + 1)
 
 
 def _empty(shape, dtype, device, stream):
@@ -518,9 +529,8 @@ def cache_append(k, v, k_cache, v_cache, block_table, seqlens, positions=None, a
     dense); block_table [N,max_pages], seqlens and positions [N], int32; acc (fp32) and pos
     (int32) [N,Hkv,slots], whose new entries become 0 and positions[n] + i (seqlens[n] + i without
     positions). seqlens and positions are not advanced."""
-    lib = _lib or load_library()
     cache, N, _, H, d, dtype, io, dev = _paged(k_cache, v_cache, block_table, seqlens)
-    cu, keep, cuh = None, None, None
+    cu, keep, cuh = 0, None, 0
     if cu_seqlens is None:
         if k.dim() != 4:
             raise ValueError("without cu_seqlens k is [B, T, Hkv, d]")
@@ -533,7 +543,8 @@ def cache_append(k, v, k_cache, v_cache, block_table, seqlens, positions=None, a
         cu = _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
         if cu_host is None or len(cu_host) != N + 1:
             raise ValueError("cu_host must hold the values of cu_seqlens")
-        keep, cuh = _host_cu(cu_host)
+        keep, _ = _host_cu(cu_host)
+        cuh = ctypes.addressof(keep)
         shape = (keep[N], H, d)
     k_p, v_p = _need("k", k, dtype, shape, dev), _need("v", v, dtype, shape, dev)
     seen_p = _may("positions", positions, torch.int32, (N,), dev)
@@ -544,7 +555,7 @@ def cache_append(k, v, k_cache, v_cache, block_table, seqlens, positions=None, a
         return
     if slots == 0 and (acc is not None or pos is not None):
         raise ValueError("acc and pos have no slots")
-    st = _call_on(dev, stream, lib.kda_cache_append, k_p, v_p, *cache, seen_p, acc_p, pos_p, slots,
+    st = _call_on(dev, stream, _APPEND, k_p, v_p, *cache, seen_p, acc_p, pos_p, slots,
                   cu, cuh, B, T, N, H, d, io)
     del keep
     if st:
@@ -575,7 +586,6 @@ def paged_decode(q, k_cache, v_cache, block_table, seqlens, scale=1.0, z=None, a
     sigmoid(z) when z [N,Hq,d] is given. acc [N,Hkv,slots] fp32 gathers the weights, summed over
     the query heads of each key-value head. max_len: host bound on seqlens (default: what
     block_table can hold, or acc's slots). Returns o [N,Hq,d]."""
-    lib = _lib or load_library()
     cache, N, page_size, H, d, dtype, io, dev = _paged(k_cache, v_cache, block_table, seqlens)
     if q.dim() != 3:
         raise ValueError("q is [N, Hq, d]")
@@ -599,8 +609,8 @@ def paged_decode(q, k_cache, v_cache, block_table, seqlens, scale=1.0, z=None, a
     if workspace is None and dev >= 0:
         workspace = _empty(paged_decode_workspace_size(N, Hq, H, d, max_len, acc is not None),
                            torch.uint8, q.device, stream)
-    ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (None, 0)
-    st = _call_on(dev, stream, lib.kda_paged_decode, q_p, *cache, z_p, scale, acc_p, slots, o_p, N,
+    ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (0, 0)
+    st = _call_on(dev, stream, _DECODE, q_p, *cache, z_p, scale, acc_p, slots, o_p, N,
                   Hq, H, d, max_len, io, ws, ws_bytes)
     if st:
         _check("kda_paged_decode", st)
@@ -622,7 +632,6 @@ def cache_evict(k_cache, v_cache, block_table, seqlens, keep, acc, pos, position
     with pos < n_first or pos >= positions[n] - n_recent stay before all others. Kept entries
     behind slot keep move into the slots that became free (K and V in place; acc and pos into
     acc_out and pos_out, by default in place too). Returns the new lengths (seqlens_out)."""
-    lib = _lib or load_library()
     cache, N, page_size, H, d, _, io, dev = _paged(k_cache, v_cache, block_table, seqlens)
     slots = acc.shape[-1] if acc is not None else 0
     shape = (N, H, slots)
@@ -643,8 +652,8 @@ def cache_evict(k_cache, v_cache, block_table, seqlens, keep, acc, pos, position
     if workspace is None and dev >= 0:
         workspace = _empty(cache_evict_workspace_size(N, H, max_len, keep), torch.uint8,
                            seqlens.device, stream)
-    ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (None, 0)
-    st = _call_on(dev, stream, lib.kda_cache_evict, *cache, seen_p, keep, n_first, n_recent, acc_p,
+    ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (0, 0)
+    st = _call_on(dev, stream, _EVICT, *cache, seen_p, keep, n_first, n_recent, acc_p,
                   pos_p, ao_p, po_p, slots, out_p, N, H, d, max_len, io, ws, ws_bytes)
     if st:
         _check("kda_cache_evict", st)

@@ -239,3 +239,66 @@ def test_binding_refuses():
         dec(max_len=1 << 32)
     with pytest.raises(TypeError, match="required"):
         kda.cache_evict(keep=8, acc=acc, pos=None, workspace=ws, **t)
+
+
+class _Words:
+    """The library with each call's arguments passed as words."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def _call(self, function, args):
+        which, pack = function
+        args = [a if a is None or isinstance(a, (int, float)) else
+                ctypes.cast(a, ctypes.c_void_p).value for a in args]
+        return self.lib.kda_paged_call(which, pack(*(a or 0 for a in args)), len(args))
+
+    def kda_cache_append(self, *a):
+        return self._call(kda._APPEND, a)
+
+    def kda_paged_decode(self, *a):
+        return self._call(kda._DECODE, a)
+
+    def kda_cache_evict(self, *a):
+        return self._call(kda._EVICT, a)
+
+
+@pytest.mark.parametrize("fn", [_append, _decode, _evict])
+def test_words_reach_the_same_checks(lib, fn):
+    """One argument wrong at a time, the direct call and the one with words refuse it alike."""
+    by_word = _Words(lib)
+    for kw in (dict(kc=None), dict(vc=MIS), dict(ps=-8), dict(ss=4), dict(hs=12), dict(np=-1),
+               dict(page=0), dict(bt=ODD), dict(mp=-1), dict(sl=None), dict(H=0),
+               dict(d=96), dict(io=7), dict(mp=1 << 28, page=64)):
+        want = fn(lib, **kw)
+        assert want in (INV, UNS), kw
+        assert fn(by_word, **kw) == want, kw
+    assert _decode(by_word, wsb=0) == _evict(by_word, ws=None) == WS
+    assert _decode(by_word, Hq=7) == _evict(by_word, nf=30, nr=8) == INV
+    assert _append(by_word, k=None) == _append(by_word, po=ODD) == INV
+
+
+@pytest.mark.parametrize("fn,ints", [
+    (_append, ("np", "page", "mp", "slots", "B", "T", "N", "H", "d", "io")),
+    (_decode, ("np", "page", "mp", "slots", "N", "Hq", "H", "d", "ml", "io")),
+    (_evict, ("np", "page", "mp", "keep", "nf", "nr", "slots", "N", "H", "d", "ml", "io"))])
+def test_words_wider_than_an_int_are_refused(lib, fn, ints):
+    """2^32 more than a size that would be taken is not cut to it. (d = 96 ends the good call.)"""
+    by_word = _Words(lib)
+    good = dict(np=8, page=16, mp=4, slots=64, B=2, T=1, N=2, H=2, d=96, io=1, Hq=8, ml=64, keep=32,
+                nf=4, nr=8)
+    assert fn(by_word, d=96) == UNS
+    for x in ints:
+        for far in (1 << 32, -(1 << 32)):
+            assert fn(by_word, **{"d": 96, x: good[x] + far}) == INV, x
+
+
+def test_words_refusals(lib):
+    for (which, pack), n in ((kda._APPEND, 25), (kda._DECODE, 25), (kda._EVICT, 28)):
+        words = pack(*[0] * n)
+        assert lib.kda_paged_call(which, words, n) == INV        # no cache
+        assert lib.kda_paged_call(which, words, n - 1) == INV
+        assert lib.kda_paged_call(which, words + words, n + 1) == INV
+        assert lib.kda_paged_call(which, None, n) == INV
+    assert lib.kda_paged_call(3, bytes(8 * 28), 28) == INV
+    assert lib.kda_paged_call(-1, bytes(8 * 28), 28) == INV
