@@ -14,8 +14,10 @@
 // radix select (11, 11 and 10 bits from the top; the blocks' histograms are summed through
 // distributed shared memory), one that counts what lies before each warp's slots, and one that
 // writes the lists of holes and of the entries that fill them. Integers only: no order of
-// atomics can show. It is bound by the latency of its dozen barriers and, for long caches, by
-// shared-memory atomics; the traffic is one read of acc and pos.
+// atomics can show. The traffic is one read of acc and pos. One sequence of 262144 slots and 8 heads
+// on 64 SMs, in thousands of cycles: 17 that read and count, 5 more counting passes, 13 barriers
+// and searches between them, 6 counting before each warp, 9 listing, 4 the last barrier. The moves
+// then take 94 us.
 // Move: the whole GPU copies the listed rows, 64 entries a block, bound by HBM (each moved row is
 // read and written once).
 #include <cooperative_groups.h>
@@ -54,7 +56,8 @@ struct SelectArgs {
 template <int kThreads, bool kMany>
 __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 1536 / kThreads) evict_select_kernel(const SelectArgs s) {
     extern __shared__ __align__(16) uint32_t s_keys[];
-    constexpr int kWarps = kThreads / 32, kAhead = 8;    // kAhead: entries a thread loads at once
+    constexpr int kWarps = kThreads / 32, kStep = 4 * kThreads;
+    constexpr int kAhead = 2;                            // steps of four slots that a thread loads ahead
     __shared__ int s_hist[3][kBins], s_coarse[3][kBins / 32];
     __shared__ int s_pick[2];
     __shared__ int s_warp[kWarps][4], s_share[4];        // counts of the warps, and of the block
@@ -84,23 +87,32 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 1536 / kThrea
         if (rank == 0 && tid == 0) s.counts[nh] = 0;
         return;
     }
-    // the block's slots [lo, hi), a warp's a contiguous run of whole kRun of them
+    // the block's slots [lo, hi), a warp's a contiguous run of whole kRun of them; hi_run: whole kRun
     const int per_warp = (len + CS * kWarps * kRun - 1) / (CS * kWarps * kRun) * kRun;
     const int lo = min(len, rank * kWarps * per_warp);
     const int hi = min(len, lo + kWarps * per_warp);
+    const int hi_run = lo + (hi - lo + kRun - 1) / kRun * kRun;
     const bool held = hi - lo <= s.keys;
-    auto key = [&](int j) { return rank_key(a.acc[at + j], a.pos[at + j], a.n_first, recent_from); };
-    // the keys of four slots from j on, j a multiple of 4; those at `end` and behind say nothing
-    auto keys4 = [&](int j, int end, uint32_t (&k)[4]) {
+    const float* acc = a.acc + at;
+    const int* pos = a.pos + at;
+    auto key = [&](int j) { return rank_key(acc[j], pos[j], a.n_first, recent_from); };
+    // The keys of four slots from j on, j a multiple of 4 below hi_run. Slots of len and behind have
+    // key 0, the lowest: as they also come last, none of the counts below can reach them before
+    // entries to be kept or moved.
+    auto keys4 = [&](int j, uint32_t (&k)[4]) {
         if (held) {
-            const uint4 v = *reinterpret_cast<const uint4*>(s_keys + (j < end ? j - lo : 0));
+            const uint4 v = *reinterpret_cast<const uint4*>(s_keys + (j - lo));
             k[0] = v.x; k[1] = v.y; k[2] = v.z; k[3] = v.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) k[i] = j + i < end ? key(j + i) : 0;
+            for (int i = 0; i < 4; ++i) k[i] = j + i < hi ? key(j + i) : 0;
         }
     };
 
+    const int keep_here = min(hi, a.keep);               // the block's slots in front end here
+    const bool wide = ((reinterpret_cast<uintptr_t>(acc) | reinterpret_cast<uintptr_t>(pos) |
+                        reinterpret_cast<uintptr_t>(a.acc_out + at) |
+                        reinterpret_cast<uintptr_t>(a.pos_out + at)) & 15) == 0;
     for (int i = tid; i < 3 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0;
     __syncthreads();
 
@@ -112,53 +124,66 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 1536 / kThrea
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);   // bits found already
-        auto count = [&](uint32_t k, bool in) {
-            in = in && (k & above) == (T & above);
-            const int digit = (int)(k >> shift) & ((1 << bits) - 1);
-            const unsigned who = __ballot_sync(0xffffffffu, in);
-            if (who == 0) return;
-            // one atomic where a warp's keys agree, as in a run of guarded or never-seen entries
-            const int lead = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
-            if (__all_sync(0xffffffffu, !in || digit == lead)) {
-                if (lane == 0) atomicAdd(&s_hist[pass][lead], __popc(who));
-            } else if (in) {
-                atomicAdd(&s_hist[pass][digit], 1);
-            }
+        // (the atomics need no help where a warp's keys agree: gathering such first cost a quarter more)
+        auto count = [&](uint32_t k) {
+            if (((k ^ T) & above) == 0) atomicAdd(&s_hist[pass][(k >> shift) & ((1u << bits) - 1)], 1);
         };
         if (pass == 0) {                                 // the one read of acc and pos
-            for (int base = lo; base < hi; base += kThreads * kAhead) {
-                float w[kAhead];
-                int q[kAhead];
+            float w[kAhead][4];
+            int q[kAhead][4];
+            auto load = [&](int j, int u) {
+                if (wide && j + 4 <= hi) {
+                    const float4 x = *reinterpret_cast<const float4*>(acc + j);
+                    const int4 y = *reinterpret_cast<const int4*>(pos + j);
+                    w[u][0] = x.x; w[u][1] = x.y; w[u][2] = x.z; w[u][3] = x.w;
+                    q[u][0] = y.x; q[u][1] = y.y; q[u][2] = y.z; q[u][3] = y.w;
+                } else {
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int j = base + u * kThreads + tid;
-                    w[u] = j < hi ? a.acc[at + j] : 0.f;
-                    q[u] = j < hi ? a.pos[at + j] : 0;
-                }
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int j = base + u * kThreads + tid;
-                    if (base + u * kThreads >= hi) break;
-                    const uint32_t k = rank_key(w[u], q[u], a.n_first, recent_from);
-                    if (j < hi && held) s_keys[j - lo] = k;
-                    if (j < hi && j < a.keep) {          // a hole's are overwritten by the move
-                        if (copy_acc) a.acc_out[at + j] = w[u];
-                        if (copy_pos) a.pos_out[at + j] = q[u];
+                    for (int i = 0; i < 4; ++i) {
+                        w[u][i] = j + i < hi ? acc[j + i] : 0.f;
+                        q[u][i] = j + i < hi ? pos[j + i] : 0;
                     }
-                    count(k, j < hi);
+                }
+            };
+            const int first = lo + 4 * tid;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) load(first + u * kStep, u);
+            for (int j0 = first; j0 < hi_run; j0 += kAhead * kStep) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int j = j0 + u * kStep;
+                    if (j >= hi_run) break;
+                    uint32_t k[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        k[i] = j + i < hi ? rank_key(w[u][i], q[u][i], a.n_first, recent_from) : 0;
+                    if (held) *reinterpret_cast<uint4*>(s_keys + (j - lo)) = make_uint4(k[0], k[1], k[2], k[3]);
+                    if (wide && j + 4 <= keep_here) {    // a hole's are overwritten by the move
+                        if (copy_acc)
+                            *reinterpret_cast<float4*>(a.acc_out + at + j) =
+                                make_float4(w[u][0], w[u][1], w[u][2], w[u][3]);
+                        if (copy_pos)
+                            *reinterpret_cast<int4*>(a.pos_out + at + j) =
+                                make_int4(q[u][0], q[u][1], q[u][2], q[u][3]);
+                    } else if (j < keep_here) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (j + i >= keep_here) break;
+                            if (copy_acc) a.acc_out[at + j + i] = w[u][i];
+                            if (copy_pos) a.pos_out[at + j + i] = q[u][i];
+                        }
+                    }
+                    load(j + kAhead * kStep, u);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) count(k[i]);
                 }
             }
         } else {
-            for (int base = lo; base < hi; base += kThreads * 4) {
-                const int j = base + tid * 4;
+            for (int j = lo + 4 * tid; j < hi_run; j += kStep) {
                 uint32_t k[4];
-                keys4(j, hi, k);
-                bool any = false;
+                keys4(j, k);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) any |= j + i < hi && (k[i] & above) == (T & above);
-                if (!__any_sync(0xffffffffu, any)) continue;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) count(k[i], j + i < hi);
+                for (int i = 0; i < 4; ++i) count(k[i]);
             }
         }
         __syncthreads();
@@ -219,16 +244,32 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 1536 / kThrea
     // A lane takes four slots at a time.
     const int w0 = min(hi, lo + warp * per_warp), w1 = min(hi, w0 + per_warp);
     int cnt[4] = {0, 0, 0, 0};                           // above in front, behind; ties in front, behind
-    for (int j = w0 + 4 * lane; j < w1; j += kRun) {
+    for (int j0 = w0; j0 < w1; j0 += kRun) {
         uint32_t k[4];
-        keys4(j, w1, k);
+        keys4(j0 + 4 * lane, k);
+        if (j0 < a.keep && j0 + kRun > a.keep) {         // keep lies within
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in = j + i < w1, front = j + i < a.keep;
-            cnt[0] += in && front && k[i] > T;
-            cnt[1] += in && !front && k[i] > T;
-            cnt[2] += in && front && k[i] == T;
-            cnt[3] += in && !front && k[i] == T;
+            for (int i = 0; i < 4; ++i) {
+                const bool front = j0 + 4 * lane + i < a.keep;
+                cnt[0] += front && k[i] > T;
+                cnt[1] += !front && k[i] > T;
+                cnt[2] += front && k[i] == T;
+                cnt[3] += !front && k[i] == T;
+            }
+        } else {
+            int up = 0, ties = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                up += k[i] > T;
+                ties += k[i] == T;
+            }
+            if (j0 < a.keep) {
+                cnt[0] += up;
+                cnt[2] += ties;
+            } else {
+                cnt[1] += up;
+                cnt[3] += ties;
+            }
         }
     }
 #pragma unroll
@@ -265,8 +306,28 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 1536 / kThrea
         if (from >= to) return;                          // (a block behind the end has no keys to read)
         for (int j0 = from & ~(kRun - 1); j0 < to; j0 += kRun) {
             const int j = j0 + 4 * lane;
-            uint32_t k[4], one[4], mine = 0;             // counts: above in the low half, ties in the high
-            keys4(j, w1, k);
+            uint32_t k[4];
+            keys4(j, k);
+            const bool tie = k[0] == T || k[1] == T || k[2] == T || k[3] == T;
+            if (j0 >= from && j0 + kRun <= to && !__any_sync(0xffffffffu, tie)) {
+                // nearly always: all of it is asked for, and it has no ties
+                const int kept = up + min(left, ties) - (kFront ? 0 : stay_f);   // before j0
+                int in_run = 0, at_list = kFront ? j0 - kept : kept;
+                bool put[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    put[i] = (k[i] > T) != kFront;
+                    const unsigned who = __ballot_sync(0xffffffffu, put[i]);
+                    at_list += __popc(who & ((1u << lane) - 1));
+                    in_run += __popc(who);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (put[i]) (kFront ? hole : tail)[at_list++] = j + i;
+                up += kFront ? kRun - in_run : in_run;
+                continue;
+            }
+            uint32_t one[4], mine = 0;                   // counts: above in the low half, ties in the high
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 one[i] = j + i < from || j + i >= to || k[i] < T ? 0u : k[i] > T ? 1u : 0x10000u;
@@ -412,15 +473,20 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     s.most = (int)most_moves(a.max_len, a.keep);
     s.counts = static_cast<int*>(a.workspace);
     s.lists = s.counts + (int64_t)a.N * a.H;
-    // a block for up to 8192 slots, 8 at most: of clusters of 16 only 7 fit the GPU at once (of 8,
-    // 15), so that the 8 heads of one long sequence took two waves of them, 60 us for 45. Shorter
-    // caches take fewer threads: fewer meet at the barriers, and more blocks share an SM.
+    // A block for up to 8192 slots, or 16384 once more blocks would outnumber the SMs (32 sequences of
+    // 32768, 8 heads: 423 us with 2 blocks a head, 433 with 4; 4 sequences of 65536: 114 with 4, 116
+    // with 8; but one of 16384: 27.6 with 2, 31.6 with 1). 8 at most: of clusters of 16 only 7 fit the
+    // GPU at once (of 8, 15), so that the 8 heads of one long sequence took two waves of them. Shorter
+    // caches take fewer threads: fewer meet at the barriers, and more blocks share an SM (64 sequences
+    // of 2000, 8 heads: 66.6 us with 256, 69.6 with 512).
+    const int64_t heads = (int64_t)a.N * a.H;
     int cluster = 1;
-    while (cluster < kMaxCluster && (int64_t)cluster * 8192 < a.max_len) cluster *= 2;
+    while (cluster < kMaxCluster && (int64_t)cluster * (heads * cluster * 2 > sm_count() ? 16384 : 8192) < a.max_len)
+        cluster *= 2;
     // A long cache alone takes all the threads that a block can have; where more blocks than SMs are
     // to run, blocks of 512 share an SM, and one's barriers overlap another's work (32 sequences of
-    // 32768, 8 heads: 508 us with 1024 threads, 452 us with 512).
-    const bool crowd = (int64_t)a.N * a.H * cluster > sm_count();
+    // 32768, 4 blocks a head: 480 us with 1024 threads, 433 with 512).
+    const bool crowd = heads * cluster > sm_count();
     const int threads = a.max_len <= 2048 ? 256 : cluster == 1 || crowd ? 512 : 1024;
     const int block = threads / 32 * kRun;               // a block's slots come in whole runs of its warps
     const int64_t need = ((int64_t)a.max_len + cluster * block - 1) / (cluster * block) * block;

@@ -478,6 +478,58 @@ def test_evict_ties_and_special_weights(kind):
     evict_case(c, 30, 2, 6)
 
 
+@pytest.mark.parametrize("length,keep", [(131, 100), (9001, 5000), (9001, 9000), (30002, 128), (30003, 16384)])
+@pytest.mark.parametrize("kind", ["nan", "steps", "runs"])
+def test_evict_threshold_among_equals(length, keep, kind):
+    """The keep-th best has equals in every warp's and block's slots; NaN is the lowest key of all,
+    and the lengths end inside a group of four slots."""
+    c = Paged("bf16", [length, length - 1, keep + 1], 1, 64, 16, seed=length + keep)
+    a = c.acc.cpu()
+    if kind == "nan":                                   # NaN entries have to stay
+        a[torch.rand(a.shape, generator=c.g) < 0.995] = float("nan")
+    elif kind == "steps":
+        a = (a * 4).floor()
+    else:
+        a = torch.arange(c.slots).div(200, rounding_mode="floor").remainder(3).float().expand_as(a)
+    c.acc = a.contiguous().to(DEV)
+    evict_case(c, keep, 3, 20)
+
+
+@pytest.mark.parametrize("off", [(0, 1, 2, 3), (1, 1, 1, 1), (4, 0, 4, 0), (0, 0, 0, 2)])
+@pytest.mark.parametrize("slots", [5000, 5002])
+def test_evict_alignment(off, slots):
+    """acc, pos and their outputs at any multiple of 4 bytes."""
+    c = Paged("bf16", [slots, 4100, 777], 3, 64, 16, seed=slots)
+    K, V, A, P = (f64(t) for t in (c.k, c.v, c.acc, c.pos))
+    want = ref.evict(K, V, c.table.numpy(), c.lens, 4001, A, P, c.lens, 4, 64)
+
+    def at(x, by):
+        room = torch.full((x.numel() + 8,), -3, dtype=x.dtype, device=DEV)
+        view = room[by:by + x.numel()].view(x.shape)
+        return room, view
+    (_, a), (_, p), (ra, ao), (rp, po) = (at(x, by) for x, by in zip((c.acc, c.pos, c.acc, c.pos), off))
+    a.copy_(c.acc)
+    p.copy_(c.pos)
+    out = kda.cache_evict(*c.args, 4001, a, p, n_first=4, n_recent=64, acc_out=ao, pos_out=po)
+    assert kda.last_device_error() == kda.KDA_OK and out.tolist() == want
+    assert np.array_equal(f64(c.k), K, equal_nan=True) and np.array_equal(f64(c.v), V, equal_nan=True)
+    for n, m in enumerate(want):
+        assert np.array_equal(f64(ao)[n, :, :m], A[n, :, :m])
+        assert np.array_equal(f64(po)[n, :, :m], P[n, :, :m])
+        assert (ao[n, :, m:] == -3).all() and (po[n, :, m:] == -3).all()
+    for room, by in ((ra, off[2]), (rp, off[3])):
+        assert (room[:by] == -3).all() and (room[by + c.acc.numel():] == -3).all()
+
+
+@pytest.mark.parametrize("longest,keep", [(12001, 5000), (20003, 16000), (40000, 10001)])
+def test_evict_more_heads_than_sms(longest, keep):
+    """Blocks then hold more slots each: 1, 2 and 4 blocks a head."""
+    g = np.random.default_rng(longest)
+    lens = [longest] + [int(x) for x in g.integers(0, 400, 78)] + [longest - 1]
+    c = Paged("bf16", lens, 2, 64, 16, seed=keep)
+    evict_case(c, keep, 5, 100)
+
+
 def test_evict_positions():
     """Guards go by position, not by slot: shuffled positions with gaps."""
     c = Paged("f32", [200, 90], 2, 64, 16, seed=12)
