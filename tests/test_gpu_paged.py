@@ -704,3 +704,36 @@ def test_c_entry_refuses_on_the_gpu_box_too():
     with pytest.raises(kda.KdaError):
         kda.cache_evict(*c.args, 4, c.acc, c.pos, n_first=3, n_recent=2)
     assert (o == 5).all()
+
+
+def test_c_entries_called_directly():
+    """The C functions with single arguments do what the calls with packed ones do."""
+    lib = kda.load_library()
+    c = Paged("bf16", [70, 0, 33], 2, 64, 16, seed=3, room=4)
+    q, z, new = c.rand(3, 4, 64), c.rand(3, 4, 64), c.rand(3, 2, 2, 64)
+    k, v, acc, pos = (t.clone() for t in (c.k, c.v, c.acc, c.pos))
+    ml = c.max_pages * c.page
+    slots = c.slots
+    p = [t.data_ptr() for t in (q, z, new, k, v, acc, pos, c.tab, c.sl)]
+    stream = torch.cuda.current_stream().cuda_stream
+    st = k.stride()[:3]
+    pages = k.shape[0]
+    sl2 = c.sl + 2
+    o, out = torch.empty_like(q), torch.empty_like(c.sl)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device=DEV)
+    ml = min(ml, slots)
+    cache = (p[3], p[4], *st, pages, 16, p[7], c.max_pages)
+    assert lib.kda_cache_append(p[2], p[2], *cache, p[8], None, p[5], p[6], slots, None, None, 3, 2, 3,
+                                2, 64, 1, stream) == kda.KDA_OK
+    assert lib.kda_paged_decode(p[0], *cache, sl2.data_ptr(), p[1], 0.2, p[5], slots, o.data_ptr(), 3,
+                                4, 2, 64, ml, 1, ws.data_ptr(), ws.numel(), stream) == kda.KDA_OK
+    assert lib.kda_cache_evict(*cache, sl2.data_ptr(), None, 20, 2, 4, p[5], p[6], p[5], p[6], slots,
+                               out.data_ptr(), 3, 2, 64, ml, 1, ws.data_ptr(), ws.numel(),
+                               stream) == kda.KDA_OK
+    kda.cache_append(new, new, *c.args, acc=c.acc, pos=c.pos)
+    o2 = kda.paged_decode(q, c.k, c.v, c.tab, sl2, scale=0.2, z=z, acc=c.acc)
+    out2 = kda.cache_evict(c.k, c.v, c.tab, sl2, 20, c.acc, c.pos, n_first=2, n_recent=4)
+    assert kda.last_device_error() == kda.KDA_OK
+    assert torch.equal(o, o2) and torch.equal(out, out2) and out.tolist() == [20, 2, 20]
+    assert torch.equal(acc, c.acc) and torch.equal(pos, c.pos)
+    assert torch.equal(k.nan_to_num(), c.k.nan_to_num()) and torch.equal(v.nan_to_num(), c.v.nan_to_num())
