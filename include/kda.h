@@ -419,7 +419,8 @@ kda_status kda_fused_recurrent_step(const void* q_raw, const void* k_raw, const 
  *  Make the first of these calls on a device before any stream capture (they look up the error word
  *  and set kernel attributes once).
  *  Not checked: that no two slots share memory (a page twice in the tables of what one call
- *  writes), and finite inputs.
+ *  writes), finite inputs, and that the sums of attention stay finite: the scores, and values times
+ *  2^8 * seqlens[n] (weights are up to 2^8 while they are summed, and divided by their sum last).
  *  Supported: d in {64, 128}, io F32 or BF16, any page_size, max_pages * page_size <= 2^30,
  *  N * max_len <= 2^36.
  */
