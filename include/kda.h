@@ -464,7 +464,8 @@ kda_status kda_paged_decode_workspace_size(int N, int Hq, int Hkv, int d, int ma
  * (kda_cache_append). Scores, softmax statistics and sums are fp32; results do not depend on
  * anything but the inputs and the device's SM count (no atomics).
  *
- *  q, z, o : [N, Hq, d] io dtype (z may be NULL); o must not overlap any input
+ *  q, z, o : [N, Hq, d] io dtype (z may be NULL); o must not overlap any input, nor the
+ *            workspace (KDA_ERR_INVALID_ARG)
  *  acc     : [N, Hkv, slots] fp32, updated in place, or NULL      slots: >= max_len with acc
  *  max_len : host bound on seqlens, <= max_pages * page_size; longer ones are clamped to it and
  *            set the error word
@@ -498,7 +499,8 @@ kda_status kda_cache_evict_workspace_size(int N, int Hkv, int max_len, int keep,
  *
  *  keep >= 0; n_first, n_recent >= 0 with n_first + n_recent <= keep
  *  acc, pos : [N, Hkv, slots]           acc_out, pos_out: the same shape, either equal to acc and
- *             pos (in place) or disjoint from them; slots >= seqlens_out[n] are not written
+ *             pos (in place) or disjoint from them (KDA_ERR_INVALID_ARG otherwise); slots >=
+ *             seqlens_out[n] are not written
  *  seqlens_out : [N] int32, may equal seqlens          max_len: as for kda_paged_decode; <= slots
  *  A page must not be reached by two sequences of the call (its rows move in place).
  *  workspace: kda_cache_evict_workspace_size() bytes, 16-byte aligned (KDA_ERR_WORKSPACE)

@@ -179,6 +179,30 @@ kda_status fill_cache(kda::PagedCache* c, const void* k_cache, const void* v_cac
     return KDA_OK;
 }
 
+// Whether [a, a + n) and [b, b + m) share bytes (an array that is not given has none).
+bool overlaps(const void* a, size_t n, const void* b, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a != nullptr && b != nullptr && n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
+// Whether [a, a + n) shares bytes with a page of k or v. What lies between the pages (those of other
+// layers, say) is not the cache's.
+bool overlaps_pages(const void* a, size_t n, const kda::PagedCache& c, int Hkv, int d, size_t esz) {
+    const __int128 most = (int64_t)1 << 61;
+    const __int128 span = ((__int128)(c.page_size - 1) * c.slot_stride +
+                           (__int128)(Hkv - 1) * c.head_stride + d) * (__int128)esz;
+    const int64_t page = (int64_t)(span < most ? span : most), stride = c.page_stride * (int64_t)esz;
+    for (const void* base : {c.k, c.v}) {
+        const int64_t from = (int64_t)(reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(base));
+        // of the pages that begin before the range's end, the last one reaches furthest
+        int64_t last = from + (int64_t)n - 1;
+        if (n == 0 || c.num_pages == 0 || last < 0) continue;
+        last = last / stride < c.num_pages ? last / stride : c.num_pages - 1;
+        if (last * stride + page > from) return true;
+    }
+    return false;
+}
+
 // Whether [a, a + n) and [b, b + n) overlap without being the same.
 bool partly_overlaps(const void* a, const void* b, size_t n) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -684,6 +708,12 @@ KDA_API kda_status kda_paged_decode(const void* q, const void* k_cache, const vo
         return KDA_ERR_UNSUPPORTED;
     if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
         return KDA_ERR_WORKSPACE;
+    const size_t esz = io == KDA_IO_BF16 ? 2 : 4, out = (size_t)N * Hq * d * esz;
+    if (overlaps(o, out, q, out) || overlaps(o, out, z, out) || overlaps(o, out, seqlens, (size_t)N * 4) ||
+        overlaps(o, out, block_table, (size_t)N * max_pages * 4) ||
+        overlaps(o, out, acc, (size_t)N * Hkv * slots * 4) || overlaps(o, out, workspace, need) ||
+        overlaps_pages(o, out, a.c, Hkv, d, esz))
+        return KDA_ERR_INVALID_ARG;
     a.c.err = device_error_word();
     if (a.c.err == nullptr) return KDA_ERR_CUDA;
     a.q = q; a.z = z;
@@ -734,6 +764,9 @@ KDA_API kda_status kda_cache_evict(void* k_cache, void* v_cache, int64_t page_st
         return KDA_ERR_UNSUPPORTED;
     if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
         return KDA_ERR_WORKSPACE;
+    if (overlaps(acc_out, side, pos, side) || overlaps(pos_out, side, acc, side) ||
+        overlaps(acc_out, side, pos_out, side))
+        return KDA_ERR_INVALID_ARG;
     a.c.err = device_error_word();
     if (a.c.err == nullptr) return KDA_ERR_CUDA;
     a.seqlens = seqlens;
