@@ -503,6 +503,8 @@ kda_status kda_cache_evict_workspace_size(int N, int Hkv, int max_len, int keep,
  *             seqlens_out[n] are not written
  *  seqlens_out : [N] int32, may equal seqlens          max_len: as for kda_paged_decode; <= slots
  *  A page must not be reached by two sequences of the call (its rows move in place).
+ *  Entries on a page out of range are ranked and moved as all others, acc and pos included; their K
+ *  and V rows count as zeros, and rows that would move to such a page are dropped.
  *  workspace: kda_cache_evict_workspace_size() bytes, 16-byte aligned (KDA_ERR_WORKSPACE)
  */
 kda_status kda_cache_evict(void* k_cache, void* v_cache, int64_t page_stride, int64_t slot_stride,

@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const SelectAr
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int r = r0 + i * kStep;
-            if (r < rows && s_from[r] >= 0 && s_to[r] >= 0) {
+            x[i] = y[i] = make_uint4(0, 0, 0, 0);        // (what a row on a bad page reads as)
+            if (r < rows && s_from[r] >= 0) {
                 x[i] = *reinterpret_cast<const uint4*>(kc + s_from[r]);
                 y[i] = *reinterpret_cast<const uint4*>(vc + s_from[r]);
             }
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const SelectAr
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int r = r0 + i * kStep;
-            if (r < rows && s_from[r] >= 0 && s_to[r] >= 0) {
+            if (r < rows && s_to[r] >= 0) {
                 *reinterpret_cast<uint4*>(kc + s_to[r]) = x[i];
                 *reinterpret_cast<uint4*>(vc + s_to[r]) = y[i];
             }
