@@ -416,8 +416,8 @@ kda_status kda_fused_recurrent_step(const void* q_raw, const void* k_raw, const 
  *  Lengths and page numbers are checked on the device: a length outside its range is clamped, and
  *  a slot whose page number is not in [0, num_pages) is left out (not attended to, not written);
  *  either sets the device error word, and kda_last_device_error then returns KDA_ERR_INDEX.
- *  Make the first of these calls on a device before any stream capture (they look up the error word
- *  and set kernel attributes once).
+ *  Make the first of these calls on a device before any stream capture (it loads the kernels).
+ *  Nothing is kept between calls, on the host or the device.
  *  Not checked: that no two slots share memory (a page twice in the tables of what one call
  *  writes), finite inputs, and that the sums of attention stay finite: the scores, and values times
  *  2^8 * seqlens[n] (weights are up to 2^8 while they are summed, and divided by their sum last).

@@ -9,7 +9,6 @@
 
 #include <string.h>
 
-#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 #include <utility>
@@ -59,18 +58,12 @@ bool cluster_prefill_path(kda_io_dtype io, int dk, int dv, int chunk) {
     return io == KDA_IO_BF16 && dk == 128 && dv == 128 && chunk == 64;
 }
 
-// Device address of the error word on the current device; cached per device.
+// Device address of the error word on the current device. Asked for every time (0.03 us): another
+// context, such as that after cudaDeviceReset, has it elsewhere.
 unsigned int* device_error_word() {
-    static std::atomic<unsigned int*> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-    unsigned int* word = dev < 64 ? known[dev].load(std::memory_order_acquire) : nullptr;
-    if (word != nullptr) return word;
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, kda::g_device_error) != cudaSuccess) return nullptr;
-    word = static_cast<unsigned int*>(p);
-    if (dev < 64) known[dev].store(word, std::memory_order_release);
-    return word;
+    return static_cast<unsigned int*>(p);
 }
 
 // A prefill split into P stretches per sequence: the layout of its workspace after the rings.

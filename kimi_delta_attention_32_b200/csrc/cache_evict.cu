@@ -434,8 +434,7 @@ int64_t most_moves(int64_t max_len, int64_t keep) {
 template <int kThreads, bool kMany>
 cudaError_t launch_select(const SelectArgs& s, int cluster, size_t smem, cudaStream_t stream) {
     auto kernel = evict_select_kernel<kThreads, kMany>;
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(kernel, sizeof(uint32_t) * kMaxKeys, allowed);
+    cudaError_t e = allow_smem(kernel, sizeof(uint32_t) * kMaxKeys);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(s.e.N * s.e.H * cluster));

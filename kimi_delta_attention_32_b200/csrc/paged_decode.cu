@@ -1079,10 +1079,9 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     p.slots = a.slots;
     // pages of a multiple of 16 slots, the common ones, need one page number a warp and no exchange
     // of row addresses between lanes
-    static std::atomic<uint64_t> allowed[2];
     const bool runs = a.c.page_size % 16 == 0;
     auto kernel = runs ? paged_decode_kernel<T, D, NT, true> : paged_decode_kernel<T, D, NT, false>;
-    cudaError_t e = allow_smem(kernel, X::kSmem, allowed[runs]);
+    cudaError_t e = allow_smem(kernel, X::kSmem);
     if (e != cudaSuccess) return e;
     // Short segments, no more than blocks, are a block each: the scan of the lengths and the joins
     // cost about five tiles' time, more than dividing gains while t tiles in sequence are no more
