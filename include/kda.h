@@ -461,8 +461,9 @@ kda_status kda_paged_decode_workspace_size(int N, int Hq, int Hkv, int d, int ma
  *     w_j = softmax_j(scale * q . K_j),   o = sum_j w_j V_j,   o *= sigmoid(z) when z is given,
  *     acc[n, hkv, j] += sum of w_j over the query heads of hkv, when acc is given.
  * A sequence of length 0 gives o = 0. The new token's own key must be in the cache already
- * (kda_cache_append). Scores, softmax statistics and sums are fp32; results do not depend on
- * anything but the inputs and the device's SM count (no atomics).
+ * (kda_cache_append). Scores, softmax statistics and sums are fp32. The same call gives the same
+ * bits (no atomics); the order of the sums follows from the sizes, seqlens, max_len and the device's
+ * SM count.
  *
  *  q, z, o : [N, Hq, d] io dtype (z may be NULL); o must not overlap any input, nor the
  *            workspace (KDA_ERR_INVALID_ARG)

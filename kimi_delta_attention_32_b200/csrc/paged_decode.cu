@@ -1084,14 +1084,19 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
     cudaError_t e = allow_smem(kernel, X::kSmem);
     if (e != cudaSuccess) return e;
     // Short segments, no more than blocks, are a block each: the scan of the lengths and the joins
-    // cost about five tiles' time, more than dividing gains while t tiles in sequence are no more
-    // than five above the t S / C of a divided block. (8 heads of one sequence: 200 slots 7.8 us
-    // whole, 8.4 divided, 512 slots 10.9 and 8.5; 128 segments: 512 slots 11.0 and 13.0, 1024 slots
-    // 17.4 and 16.3.) max_len may be far above the lengths, whose balance the division keeps: 16 at
-    // most.
+    // cost as much as some tiles, more than dividing gains while t tiles in sequence are no more
+    // than that above the t S / C of a divided block. Of bf16's tiles it is five, of fp32's, which take
+    // longer, three and a half with rows of 256 bytes and two and a half with 512. Whole and divided,
+    // us, 8 segments: bf16, 128 channels, 4 tiles 11.4 and 13.6, 8 tiles 15.4 and 13.6; fp32, 64
+    // channels, 3 tiles 11.3 and 13.1, 5 tiles 14.8 and 13.1; fp32, 128 channels, 2 tiles 13.5 and 14.8,
+    // 4 tiles 19.3 and 15.0 (16 heads: 24.4 and 18.9). 128 segments of 8 tiles: 15.5 and 21.0, 18.9 and
+    // 22.9, 34.8 and 41.6. With weights gathered the whole form gains 2 to 4 us less; the rule does not
+    // go by that, so that the outputs are the same with them and without. max_len may be far above
+    // the lengths, whose balance the division keeps: 16 at most.
     const int64_t segments = (int64_t)a.N * a.H * p.GT, blocks = p.most_blocks;
     const int64_t t = (a.max_len + X::kTile - 1) / X::kTile;
-    p.whole = segments <= blocks && t <= 16 && t * (blocks - segments) <= 5 * blocks ? (int)t : 0;
+    const int half_tiles = X::kBf16 ? 10 : X::kRowBytes == 256 ? 7 : 5;
+    p.whole = segments <= blocks && t <= 16 && 2 * t * (blocks - segments) <= half_tiles * blocks ? (int)t : 0;
     kernel<<<p.whole > 0 ? (unsigned)segments : p.most_blocks, X::W * 32, X::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.whole > 0 && a.acc == nullptr) return cudaSuccess;

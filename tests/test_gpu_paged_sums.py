@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from kimi_delta_attention_32_b200 import kda
+from test_gpu_paged import Paged, check_decode
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -46,3 +47,15 @@ def test_long_sums_do_not_drift(d):
     o = kda.paged_decode(q, torch.zeros_like(vc), vc, table, lens)
     assert kda.last_device_error() == kda.KDA_OK
     assert torch.equal(o, torch.full_like(o, 1 + 2.0 ** -7)), o.double().mean().item()
+
+
+@pytest.mark.parametrize("io,d,tile", [("bf16", 128, 64), ("bf16", 64, 64), ("f32", 64, 64), ("f32", 128, 128)])
+@pytest.mark.parametrize("tiles", [2, 3, 4, 5, 6])
+def test_outputs_do_not_depend_on_the_weights_being_gathered(io, d, tile, tiles):
+    """On both sides of the length up to which a block takes a whole segment."""
+    c = Paged(io, [tile * tiles, tile * tiles - 5, 1], 2, d, 16, seed=tiles)
+    q = c.rand(3, 8, d)
+    acc = c.acc.clone()
+    o = kda.paged_decode(q, *c.args, scale=0.2, acc=acc, max_len=tile * tiles)
+    check_decode(c, q, o, 0.2, None, acc, c.acc)
+    assert torch.equal(o, kda.paged_decode(q, *c.args, scale=0.2, max_len=tile * tiles))
