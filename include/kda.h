@@ -421,8 +421,14 @@ kda_status kda_fused_recurrent_step(const void* q_raw, const void* k_raw, const 
  *  Not checked: that no two slots share memory (a page twice in the tables of what one call
  *  writes), finite inputs, and that the sums of attention stay finite: the scores, and values times
  *  2^8 * seqlens[n] (weights are up to 2^8 while they are summed, and divided by their sum last).
- *  Supported: d in {64, 128}, io F32 or BF16, any page_size, max_pages * page_size <= 2^30,
- *  N * max_len <= 2^36.
+ *  Supported (KDA_ERR_UNSUPPORTED otherwise): d in {64, 128}, io F32 or BF16, any page_size,
+ *  max_pages * page_size <= 2^30, strides below 2^31 * 16 bytes, N * Hkv < 2^31; T_tot < 2^31 for
+ *  kda_cache_append; N * Hq and N * (max_len / 64 + 1) < 2^31 for kda_paged_decode; 8 * N * Hkv and
+ *  N * Hkv * ceil(min(keep, max_len - keep) / 64) < 2^31 for kda_cache_evict.
+ *  max_len, the host's bound on seqlens, costs nothing in kda_paged_decode without acc. With acc the
+ *  workspace holds 4 bytes a query head and slot of it (4 N Hq max_len), and it takes time there
+ *  and in kda_cache_evict: 32 sequences of about 4000 slots, 8 heads, attend in 119, 121, 137 and
+ *  197 us with a bound of 1, 4, 16 and 64 times the longest, and are cut in 23, 41, 72 and 133.
  */
 
 /*

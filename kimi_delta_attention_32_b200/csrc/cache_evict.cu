@@ -10,7 +10,8 @@
 //
 // Select: one thread-block cluster per (sequence, head), of 1 to 8 blocks by the cache's length.
 // Each block reads its part of acc and pos once, into 32-bit keys in shared memory (up to 49152 a
-// block; longer caches are read again in every pass), and all passes run on those: three of a
+// block; with a bound max_len above 393216 none are held, and acc and pos are read again in every
+// pass), and all passes run on those: three of a
 // radix select (11, 11 and 10 bits from the top; the blocks' histograms are summed through
 // distributed shared memory), one that counts what lies before each warp's slots, and one that
 // writes the lists of holes and of the entries that fill them. Integers only: no order of

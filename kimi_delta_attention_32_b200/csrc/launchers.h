@@ -157,7 +157,7 @@ struct AppendArgs {
     PagedCache c;
     const void *k, *v;               // [T_tot, H, d]
     const int32_t* seqlens;
-    const int32_t* positions;        // or null: seqlens
+    const int32_t* positions;
     float* acc;                      // [N, H, slots] or null
     int32_t* pos;                    // [N, H, slots] or null
     int slots;

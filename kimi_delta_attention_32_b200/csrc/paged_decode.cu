@@ -48,7 +48,7 @@ namespace kda {
 namespace {
 
 constexpr int kMaxBlocks = 480;          // blocks of one launch: 3 an SM, for up to 160 SMs
-constexpr float kSlack = 8.f;            // a score may exceed the running maximum by 2^8
+constexpr float kSlack = 8.f;            // log2: a weight may reach 2^8 before the running maximum moves
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
