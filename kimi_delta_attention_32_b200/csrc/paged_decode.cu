@@ -91,29 +91,22 @@ __device__ __forceinline__ void mma_tf32(float* d, const uint32_t* a, uint32_t b
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // x = hi + lo up to 2^-21 x, both TF32 values (fp32 with 10 bits of fraction): hi is rounded to
-// the nearest, so |lo| <= 2^-11 x, and lo is cut. Four operations, fewer than two conversions take;
-// a fifth keeps hi of values from (2 - 2^-11) 2^127 on, which would round to infinity, at the largest
-// TF32 (weights, kSmall, are never that large; 0 to 3% of a call). An infinite x is then lo's.
-template <bool kSmall>
+// the nearest, so |lo| <= 2^-11 x, and lo is cut. Values from (2 - 2^-11) 2^127 on would round to
+// infinity: hi then is the largest TF32, and an infinite x is lo's. (Rounded by two integer operations
+// instead, without that limit, 32 sequences of 4096, 32/8 heads of 128, took 171 us, 167 this way.)
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
-    hi = (x + 0x1000u) & 0xffffe000u;
-    if constexpr (!kSmall) {
-        float h;                                       // the smaller magnitude, with hi's sign
-        asm("min.xorsign.abs.f32 %0, %1, 0f7F7FE000;" : "=f"(h) : "f"(__uint_as_float(hi)));
-        hi = __float_as_uint(h);
-    }
+    asm("cvt.rn.satfinite.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
     lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) & 0xffffe000u;
 }
 // d += a b to fp32's accuracy: the two small cross products, then the large one, summed from zero
 // and added to d in fp32 (1.8e-6 of the output was measured with the tensor cores' running sums over a
-// long cache, 2.4e-7 this way). kWeights: b holds softmax weights.
-template <bool kWeights>
+// long cache, 2.4e-7 this way).
 __device__ __forceinline__ void mma_f32(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
     uint32_t ah[4], al[4], bh0, bh1, bl0, bl1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split_tf32<false>(a[i], ah[i], al[i]);
-    split_tf32<kWeights>(b0, bh0, bl0);
-    split_tf32<kWeights>(b1, bh1, bl1);
+    for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
+    split_tf32(b0, bh0, bl0);
+    split_tf32(b1, bh1, bl1);
     float t[4] = {0.f, 0.f, 0.f, 0.f};
     mma_tf32(t, al, bh0, bh1);
     mma_tf32(t, ah, bl0, bl1);
@@ -576,8 +569,8 @@ paged_decode_kernel(const Params p) {
                     mma_bf16(s[nt], a0, bq[0], bq[1]);
                     mma_bf16(kTwo ? s2[kTwo ? nt : 0] : s[nt], a1, bq[2], bq[3]);
                 } else {
-                    mma_f32<false>(s[nt], a0, bq[0], bq[1]);
-                    mma_f32<false>(kTwo ? s2[kTwo ? nt : 0] : s[nt], a1, bq[2], bq[3]);
+                    mma_f32(s[nt], a0, bq[0], bq[1]);
+                    mma_f32(kTwo ? s2[kTwo ? nt : 0] : s[nt], a1, bq[2], bq[3]);
                 }
             }
         }
@@ -689,8 +682,8 @@ paged_decode_kernel(const Params p) {
                     const uint32_t a0[4] = {x.x, x.y, y.x, y.y}, a1[4] = {x.z, x.w, y.z, y.w};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_f32<true>(out[nt][2 * pc], a0, pb[nt][0], pb[nt][1]);
-                        mma_f32<true>(out[nt][2 * pc + 1], a1, pb[nt][0], pb[nt][1]);
+                        mma_f32(out[nt][2 * pc], a0, pb[nt][0], pb[nt][1]);
+                        mma_f32(out[nt][2 * pc + 1], a1, pb[nt][0], pb[nt][1]);
                     }
                 }
             }
